@@ -11,6 +11,8 @@
 
 #include "attn.cuh"
 #include "decode.cuh"
+#include "kv8.cuh"
+#include "linear.cuh"
 #include "qat.cuh"
 #include "select.cuh"
 
@@ -624,6 +626,75 @@ thrift_status decode_impl(const void* q, int B, int H, int Hkv, int capacity, co
   if (s != THRIFT_OK) return s;
   dec_combine_kernel<DT><<<B * H, kDecD, 0, st>>>(w.part_o, w.part_ml, 2 * p.nsplit,
                                                   static_cast<uint16_t*>(out), lse);
+  return launch_status();
+}
+
+// ------------------------------------------------------------ 8-bit cache --
+
+thrift_status kv8_shape(int B, int Hkv, int d, int blk, int capacity) {
+  if (B <= 0 || Hkv <= 0 || d <= 0 || blk <= 0 || capacity <= 0) return THRIFT_ERR_ARG;
+  if ((d != 64 && d != 128) || (blk != 16 && blk != 32 && blk != 64 && blk != 128))
+    return THRIFT_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || capacity > (1 << 30)) return THRIFT_ERR_UNSUPPORTED;
+  return THRIFT_OK;
+}
+
+// Whether the strides (bytes) of [B, Hkv, capacity, d] codes are multiples of
+// 16 under which no two rows overlap; `extent` is what they span.
+bool kv8_strides_ok(int B, int Hkv, int d, int capacity, int64_t sb, int64_t sh, int64_t st,
+                    int64_t* extent) {
+  std::pair<int64_t, int64_t> dim[3];  // stride, size
+  int n = 0;
+  if (B > 1) dim[n++] = {sb, B};
+  if (Hkv > 1) dim[n++] = {sh, Hkv};
+  if (capacity > 1) dim[n++] = {st, capacity};
+  std::sort(dim, dim + n);
+  int64_t span = d;
+  for (int i = 0; i < n; ++i) {
+    if (dim[i].first < span || dim[i].first % 16 || dim[i].first >= ((int64_t)1 << 40)) return false;
+    span += dim[i].first * (dim[i].second - 1);
+  }
+  *extent = span;
+  return true;
+}
+
+Kv8Geom kv8_geom(int B, int Hkv, int blk, int capacity, int64_t sb, int64_t sh, int64_t st) {
+  return Kv8Geom{B, Hkv, capacity, blk, (int)ceil_div(capacity, blk), sb, sh, st};
+}
+
+bool ranges_meet(const void* a, int64_t an, const void* b, int64_t bn) {
+  const char* x = static_cast<const char*>(a);
+  const char* y = static_cast<const char*>(b);
+  return x < y + bn && y < x + an;
+}
+
+template <int DT, int D>
+thrift_status kv8_append_impl(const void* kn, const void* vn, const Kv8Geom& g, int max_new,
+                              const int32_t* cache_len, const int32_t* n_new, void* k, void* v,
+                              float* ks, float* vs, float* weight, int32_t* new_len,
+                              cudaStream_t st) {
+  const int nb = (int)ceil_div((int64_t)max_new - 1, g.blk) + 1;  // blocks max_new tokens can touch
+  kv8_append_kernel<DT, D><<<dim3(nb, g.Hkv, g.B), kKv8Threads, 0, st>>>(
+      static_cast<const uint16_t*>(kn), static_cast<const uint16_t*>(vn), g, max_new, cache_len,
+      n_new, static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), ks, vs, weight);
+  if (new_len)
+    kv8_advance_kernel<<<(int)ceil_div(g.B, kThreads), kThreads, 0, st>>>(g, max_new, cache_len,
+                                                                         n_new, new_len);
+  return launch_status();
+}
+
+template <int DT, int D>
+thrift_status kv8_decode_impl(const void* q, const Kv8Geom& g, int H, const void* k, const void* v,
+                              const float* ks, const float* vs, const int32_t* seq_len, float scale,
+                              float* weight, void* out, float* lse, cudaStream_t st) {
+  const uint16_t* qp = static_cast<const uint16_t*>(q);
+  const uint8_t* kp = static_cast<const uint8_t*>(k);
+  kv8_decode_kernel<DT, D><<<dim3(H, g.B), 128, 0, st>>>(
+      qp, g, H, kp, static_cast<const uint8_t*>(v), ks, vs, seq_len, scale,
+      static_cast<uint16_t*>(out), lse);
+  if (weight)
+    kv8_weight_kernel<DT, D><<<dim3((unsigned)ceil_div(g.capacity, 128), g.Hkv, g.B), 128, 0, st>>>(
+        qp, g, H, kp, ks, seq_len, scale, lse, weight);
   return launch_status();
 }
 
@@ -1276,6 +1347,160 @@ thrift_status thrift_qat_bwd_varlen(const void* q, const void* k, const void* v,
   if (!reuse_images)
     s = qat_images<0>(q, k, v, si, nseq, total, max_seqlen, H, Hkv, d, use_scalesearch, w, st);
   return s != THRIFT_OK ? s : qat_bwd_dispatch<0>(p, dout, nseq, max_seqlen, d, blk, st);
+}
+
+// --------------------------------------------------------- 8-bit cache --
+
+thrift_status thrift_kv8_append(const void* k_new, const void* v_new, thrift_dtype dt, int B,
+                                int Hkv, int d, int blk, int capacity, int64_t stride_b,
+                                int64_t stride_h, int64_t stride_t, const int32_t* cache_len,
+                                const int32_t* n_new, int max_new, void* k, void* v,
+                                float* k_scale, float* v_scale, float* weight, int32_t* new_len,
+                                void* stream) {
+  thrift_status s = kv8_shape(B, Hkv, d, blk, capacity);
+  if (s != THRIFT_OK) return s;
+  if (dt != THRIFT_F16 && dt != THRIFT_BF16) return THRIFT_ERR_ARG;
+  if (max_new < 0 || max_new > (1 << 30)) return THRIFT_ERR_ARG;
+  if (!cache_len || !k || !v || !k_scale || !v_scale || !aligned16(k) || !aligned16(v))
+    return THRIFT_ERR_ARG;
+  if (max_new > 0 && (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)))
+    return THRIFT_ERR_ARG;
+  int64_t extent;
+  if (!kv8_strides_ok(B, Hkv, d, capacity, stride_b, stride_h, stride_t, &extent) || k == v)
+    return THRIFT_ERR_ARG;
+  const Kv8Geom g = kv8_geom(B, Hkv, blk, capacity, stride_b, stride_h, stride_t);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (max_new == 0) {
+    if (!new_len) return THRIFT_OK;
+    kv8_advance_kernel<<<(int)ceil_div(B, kThreads), kThreads, 0, st>>>(g, 0, cache_len, nullptr,
+                                                                       new_len);
+    return launch_status();
+  }
+  const auto run = dt == THRIFT_BF16 ? (d == 128 ? kv8_append_impl<1, 128> : kv8_append_impl<1, 64>)
+                                     : (d == 128 ? kv8_append_impl<0, 128> : kv8_append_impl<0, 64>);
+  return run(k_new, v_new, g, max_new, cache_len, n_new, k, v, k_scale, v_scale, weight, new_len,
+             st);
+}
+
+size_t thrift_kv8_decode_workspace_size(int B, int H, int Hkv, int capacity, int d,
+                                        int accumulate) {
+  if (kv8_shape(B, Hkv, d, 16, capacity) != THRIFT_OK || H <= 0 || H % Hkv) return 0;
+  (void)accumulate;
+  return 256;
+}
+
+thrift_status thrift_kv8_decode(const void* q, thrift_dtype dt, int B, int H, int Hkv, int d,
+                                int blk, int capacity, int64_t stride_b, int64_t stride_h,
+                                int64_t stride_t, const void* k, const void* v,
+                                const float* k_scale, const float* v_scale,
+                                const int32_t* seq_len, float scale, float* weight, void* out,
+                                float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  thrift_status s = kv8_shape(B, Hkv, d, blk, capacity);
+  if (s != THRIFT_OK) return s;
+  if (dt != THRIFT_F16 && dt != THRIFT_BF16) return THRIFT_ERR_ARG;
+  if (H <= 0 || H % Hkv || !(std::fabs(scale) <= 3.0e38f)) return THRIFT_ERR_ARG;
+  if (!q || !k || !v || !k_scale || !v_scale || !seq_len || !out || !lse || !workspace)
+    return THRIFT_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
+    return THRIFT_ERR_ARG;
+  int64_t extent;
+  if (!kv8_strides_ok(B, Hkv, d, capacity, stride_b, stride_h, stride_t, &extent))
+    return THRIFT_ERR_ARG;
+  if (ws_bytes < thrift_kv8_decode_workspace_size(B, H, Hkv, capacity, d, weight != nullptr))
+    return THRIFT_ERR_ARG;
+  const Kv8Geom g = kv8_geom(B, Hkv, blk, capacity, stride_b, stride_h, stride_t);
+  const auto run = dt == THRIFT_BF16 ? (d == 128 ? kv8_decode_impl<1, 128> : kv8_decode_impl<1, 64>)
+                                     : (d == 128 ? kv8_decode_impl<0, 128> : kv8_decode_impl<0, 64>);
+  return run(q, g, H, k, v, k_scale, v_scale, seq_len, scale, weight, out, lse,
+             static_cast<cudaStream_t>(stream));
+}
+
+size_t thrift_kv8_evict_workspace_size(int B, int Hkv, int capacity, int budget) {
+  if (B <= 0 || Hkv <= 0 || capacity <= 0 || budget <= 0) return 0;
+  return (size_t)B * Hkv * std::min(budget, capacity) * sizeof(int32_t);
+}
+
+thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int64_t stride_b,
+                               int64_t stride_h, int64_t stride_t, const void* k, const void* v,
+                               const float* k_scale, const float* v_scale, const float* weight,
+                               const int32_t* seq_len, int budget, int sink, int recent,
+                               int out_capacity, int64_t out_stride_b, int64_t out_stride_h,
+                               int64_t out_stride_t, void* k_out, void* v_out, float* k_scale_out,
+                               float* v_scale_out, float* weight_out, int32_t* len_out,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  thrift_status s = kv8_shape(B, Hkv, d, blk, capacity);
+  if (s == THRIFT_OK) s = kv8_shape(B, Hkv, d, blk, out_capacity);
+  if (s != THRIFT_OK) return s;
+  if (budget <= 0 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
+    return THRIFT_ERR_ARG;
+  budget = std::min(budget, capacity);  // no sequence is longer than its cache
+  if (out_capacity < budget) return THRIFT_ERR_ARG;
+  if (!k || !v || !k_scale || !v_scale || !weight || !seq_len || !k_out || !v_out ||
+      !k_scale_out || !v_scale_out || !weight_out || !len_out || !workspace)
+    return THRIFT_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_out) || !aligned16(v_out) ||
+      !aligned16(workspace))
+    return THRIFT_ERR_ARG;
+  int64_t in_n, out_n;
+  if (!kv8_strides_ok(B, Hkv, d, capacity, stride_b, stride_h, stride_t, &in_n) ||
+      !kv8_strides_ok(B, Hkv, d, out_capacity, out_stride_b, out_stride_h, out_stride_t, &out_n))
+    return THRIFT_ERR_ARG;
+  // the survivors are gathered in parallel: nothing read may be written
+  const int64_t pairs = (int64_t)B * Hkv;
+  const int64_t sc = pairs * ceil_div(capacity, blk) * 4, sco = pairs * ceil_div(out_capacity, blk) * 4;
+  const std::pair<const void*, int64_t> in[] = {
+      {k, in_n}, {v, in_n}, {k_scale, sc}, {v_scale, sc}, {weight, pairs * capacity * 4},
+      {seq_len, (int64_t)B * 4}};
+  const std::pair<const void*, int64_t> to[] = {
+      {k_out, out_n}, {v_out, out_n}, {k_scale_out, sco}, {v_scale_out, sco},
+      {weight_out, pairs * out_capacity * 4}, {len_out, (int64_t)B * 4}};
+  for (const auto& a : in)
+    for (const auto& b : to)
+      if (ranges_meet(a.first, a.second, b.first, b.second)) return THRIFT_ERR_ARG;
+  if (k_out == v_out || ws_bytes < thrift_kv8_evict_workspace_size(B, Hkv, capacity, budget))
+    return THRIFT_ERR_ARG;
+  const Kv8Geom g = kv8_geom(B, Hkv, blk, capacity, stride_b, stride_h, stride_t);
+  const Kv8Geom go =
+      kv8_geom(B, Hkv, blk, out_capacity, out_stride_b, out_stride_h, out_stride_t);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t* kept = static_cast<int32_t*>(workspace);
+  kv8_select_kernel<<<dim3(Hkv, B), kKv8SelThreads, 0, st>>>(weight, g, seq_len, budget, sink,
+                                                             recent, kept, len_out);
+  const dim3 grid((unsigned)ceil_div(budget, blk), Hkv, B);
+  const auto gather = d == 128 ? kv8_gather_kernel<128> : kv8_gather_kernel<64>;
+  gather<<<grid, kKv8Threads, 0, st>>>(
+      g, go, static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_scale, v_scale,
+      weight, seq_len, kept, budget, static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out),
+      k_scale_out, v_scale_out, weight_out);
+  return launch_status();
+}
+
+// -------------------------------------------------------------- linear --
+
+size_t nvfp4_linear_workspace_size(int M, int64_t N, int K) {
+  if (M <= 0 || M > kLinMaxM || N <= 0 || K <= 0 || K % 32) return 0;
+  return 256;
+}
+
+thrift_status nvfp4_linear(const void* x, thrift_dtype dt, int M, int64_t N, int K,
+                           const uint8_t* codes, const uint8_t* scales,
+                           const float* tensor_scale, void* out, void* workspace, size_t ws_bytes,
+                           void* stream) {
+  if (dt != THRIFT_F16 && dt != THRIFT_BF16) return THRIFT_ERR_ARG;
+  if (M < 0 || N < 0 || K <= 0 || K % 16) return THRIFT_ERR_ARG;
+  if (M > kLinMaxM || K % 32 || N > (1 << 30) || K > (1 << 24)) return THRIFT_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return THRIFT_OK;
+  if (!x || !codes || !scales || !tensor_scale || !out || !workspace) return THRIFT_ERR_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(out) ||
+      !aligned16(workspace))
+    return THRIFT_ERR_ARG;
+  if (ws_bytes < nvfp4_linear_workspace_size(M, N, K)) return THRIFT_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)ceil_div(N, 8);
+  const auto kernel = dt == THRIFT_BF16 ? linear_kernel<1> : linear_kernel<0>;
+  kernel<<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x), M, K, (int)N, codes, scales,
+                               tensor_scale, static_cast<uint16_t*>(out));
+  return launch_status();
 }
 
 }  // extern "C"

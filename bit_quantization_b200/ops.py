@@ -32,6 +32,9 @@ EXPORTS = (
     "thrift_kernel_timer_enable", "thrift_kernel_timer_read", "thrift_test_wait_timeout",
     "thrift_kv_cache_size", "thrift_kv_cache_append", "thrift_attn_decode_workspace_size",
     "thrift_attn_decode_mask_offset", "thrift_attn_decode",
+    "thrift_kv8_append", "thrift_kv8_decode_workspace_size", "thrift_kv8_decode",
+    "thrift_kv8_evict_workspace_size", "thrift_kv8_evict",
+    "nvfp4_linear_workspace_size", "nvfp4_linear",
     "thrift_qat_workspace_size", "thrift_qat_fwd_varlen", "thrift_qat_bwd_varlen",
 )
 
@@ -113,6 +116,24 @@ def lib():
         L.thrift_qat_bwd_varlen.restype = i32
         L.thrift_qat_bwd_varlen.argtypes = [P, P, P, P, i32, P, i32, i64, i32, i32, i32, i32, i32,
                                             i32, i32, i32, P, P, P, P, P, P, sz, P]
+        L.thrift_kv8_append.restype = i32
+        L.thrift_kv8_append.argtypes = [P, P, i32, i32, i32, i32, i32, i32, i64, i64, i64, P, P,
+                                        i32, P, P, P, P, P, P, P]
+        L.thrift_kv8_decode_workspace_size.restype = sz
+        L.thrift_kv8_decode_workspace_size.argtypes = [i32] * 6
+        L.thrift_kv8_decode.restype = i32
+        L.thrift_kv8_decode.argtypes = [P, i32, i32, i32, i32, i32, i32, i32, i64, i64, i64, P, P,
+                                        P, P, P, f32, P, P, P, P, sz, P]
+        L.thrift_kv8_evict_workspace_size.restype = sz
+        L.thrift_kv8_evict_workspace_size.argtypes = [i32] * 4
+        L.thrift_kv8_evict.restype = i32
+        L.thrift_kv8_evict.argtypes = [i32, i32, i32, i32, i32, i64, i64, i64, P, P, P, P, P, P,
+                                       i32, i32, i32, i32, i64, i64, i64, P, P, P, P, P, P, P, sz,
+                                       P]
+        L.nvfp4_linear_workspace_size.restype = sz
+        L.nvfp4_linear_workspace_size.argtypes = [i32, i64, i32]
+        L.nvfp4_linear.restype = i32
+        L.nvfp4_linear.argtypes = [P, i32, i32, i64, i32, P, P, P, P, P, sz, P]
         _lib = L
     return _lib
 
@@ -584,6 +605,244 @@ def thrift_attn_decode(q, cache: DoubleKVCache, topk_frac=0.0, sink_blocks=0, re
                                         _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(q)),
                "thrift_attn_decode")
     return out, lse
+
+
+# ----------------------------------------------------------- 8-bit cache --
+
+_F8 = torch.float8_e4m3fn
+
+
+def _same_device(first, *ts):
+    """Every given tensor on the CUDA device of the first."""
+    if not first.is_cuda:
+        raise ThriftError("tensors must live on a CUDA device")
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ThriftError(f"tensors must live on one device: {t.device} and {first.device}")
+
+
+def _vector(t, n, dtype, name):
+    """A contiguous auxiliary tensor of n elements."""
+    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+        raise ThriftError(f"{name} must be contiguous {dtype} with {n} elements, got {t.dtype} "
+                          f"{tuple(t.shape)}")
+
+
+def _scratch(nbytes, device):
+    """Workspace of a call: the stream's own buffer, or, under graph capture,
+    memory of the graph's pool (two graphs never share it, and it lives as
+    long as the graph)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    return _ws.get(nbytes, device)
+
+
+def _kv8_cache(k, v, k_scale, v_scale, blk, what=""):
+    """Checks the four tensors of an 8-bit cache; returns B, Hkv, capacity, d
+    and the codes' strides (batch, head, token) in bytes."""
+    if k.dim() != 4 or k.dtype != _F8 or v.dtype != _F8 or v.shape != k.shape:
+        raise ThriftError(f"k{what}, v{what} must be {_F8} [B, Hkv, capacity, d] of one shape")
+    if k.stride() != v.stride() or k.stride(3) != 1:
+        raise ThriftError(f"k{what}, v{what} must have one layout, the last axis contiguous")
+    B, Hkv, cap, d = k.shape
+    if blk not in (16, 32, 64, 128) or d not in (64, 128):
+        raise ThriftError("the 8-bit cache supports blk 16, 32, 64, 128 and d 64, 128")
+    shape = (B, Hkv, -(-cap // blk))
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check_like(t, shape, torch.float32, name + what)
+        if not t.is_contiguous():
+            raise ThriftError(f"{name}{what} must be contiguous")
+    return B, Hkv, cap, d, k.stride()[:3]
+
+
+def thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new=None, blk=64,
+                      weight=None, new_len=None):
+    """Appends k_new, v_new [B, T, Hkv, d] (n_new int32 [B] of them, default
+    all) behind ``cache_len`` (int32 [B], device) to the 8-bit cache k, v
+    (float8_e4m3fn [B, Hkv, capacity, d], any strides with the last axis
+    contiguous), k_scale, v_scale (f32 [B, Hkv, ceil(capacity / blk)]).
+    ``weight`` (f32 [B, Hkv, capacity]) is zeroed for the new tokens;
+    ``new_len`` (int32 [B], may be ``cache_len``) receives the new lengths."""
+    B, Hkv, cap, d, st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[0] != B or \
+            k_new.shape[2:] != (Hkv, d):
+        raise ThriftError(f"k_new, v_new must both be [{B}, T, {Hkv}, {d}]")
+    if k_new.dtype != v_new.dtype:
+        raise ThriftError("k_new and v_new differ in dtype")
+    _vector(cache_len, B, torch.int32, "cache_len")
+    _vector(n_new, B, torch.int32, "n_new")
+    _vector(new_len, B, torch.int32, "new_len")
+    _vector(weight, B * Hkv * cap, torch.float32, "weight")
+    _same_device(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new, weight, new_len)
+    _need_cuda(k_new, v_new)
+    with _on(k_new):
+        _check(lib().thrift_kv8_append(_ptr(k_new), _ptr(v_new), _dt(k_new), B, Hkv, d, blk, cap,
+                                       *st, _ptr(cache_len), _ptr(n_new), k_new.shape[1], _ptr(k),
+                                       _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight),
+                                       _ptr(new_len), _stream(k_new)), "thrift_kv8_append")
+
+
+def kv8_decode_workspace_size(B, H, Hkv, capacity, d=128, accumulate=False) -> int:
+    return int(lib().thrift_kv8_decode_workspace_size(B, H, Hkv, capacity, d, int(accumulate)))
+
+
+def thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk=64, scale=None, weight=None,
+                      out=None, lse=None, workspace=None):
+    """q [B,H,d] -> (out [B,H,d], lse f32 [B,H]) over the ``seq_len`` (int32
+    [B], device) cached tokens of an 8-bit cache (see thrift_kv8_append);
+    ``scale`` defaults to 1/sqrt(d).  ``weight`` (f32 [B, Hkv, capacity])
+    accumulates each token's probability, summed over the query heads of its
+    kv head."""
+    B, Hkv, cap, d, st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % Hkv:
+        raise ThriftError(f"q must be [{B}, H (a multiple of {Hkv}), {d}]")
+    H = q.shape[1]
+    _check_like(out, q.shape, q.dtype, "out")
+    _check_like(lse, (B, H), torch.float32, "lse")
+    _vector(seq_len, B, torch.int32, "seq_len")
+    _vector(weight, B * Hkv * cap, torch.float32, "weight")
+    _same_device(q, k, v, k_scale, v_scale, seq_len, weight, out, lse, workspace)
+    _need_cuda(q, *(t for t in (out, lse, workspace) if t is not None))
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    with _on(q):
+        if workspace is None:
+            need = kv8_decode_workspace_size(B, H, Hkv, cap, d, weight is not None)
+            workspace = _scratch(need, q.device)
+        _check(lib().thrift_kv8_decode(_ptr(q), _dt(q), B, H, Hkv, d, blk, cap, *st, _ptr(k),
+                                       _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(seq_len),
+                                       d ** -0.5 if scale is None else float(scale), _ptr(weight),
+                                       _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                       _stream(q)), "thrift_kv8_decode")
+    return out, lse
+
+
+def kv8_evict_workspace_size(B, Hkv, capacity, budget) -> int:
+    return int(lib().thrift_kv8_evict_workspace_size(B, Hkv, capacity, budget))
+
+
+def thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_out, k_scale_out,
+                     v_scale_out, weight_out, len_out, blk=64, recent=0, sink=0, workspace=None):
+    """Writes into a second 8-bit cache (``*_out``, apart from the first) what
+    stays of each (sequence, kv head) when its tokens are cut to ``budget``:
+    the first ``sink``, the last ``recent`` and the heaviest others by
+    ``weight``, in their order; ``len_out`` = min(seq_len, budget)."""
+    B, Hkv, cap, d, st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    Bo, Ho, cap_o, do, sto = _kv8_cache(k_out, v_out, k_scale_out, v_scale_out, blk, "_out")
+    if (Bo, Ho, do) != (B, Hkv, d):
+        raise ThriftError("the two caches must agree in batch, heads and d")
+    budget, recent, sink = int(budget), int(recent), int(sink)
+    if budget < 1 or recent < 0 or sink < 0 or sink + recent > budget:
+        raise ThriftError("budget must be positive and at least sink + recent")
+    if cap_o < min(budget, cap):
+        raise ThriftError(f"the cache written to holds {cap_o} tokens, the budget is {budget}")
+    _vector(weight, B * Hkv * cap, torch.float32, "weight")
+    _vector(weight_out, B * Hkv * cap_o, torch.float32, "weight_out")
+    _vector(seq_len, B, torch.int32, "seq_len")
+    _vector(len_out, B, torch.int32, "len_out")
+    _same_device(k, v, k_scale, v_scale, weight, seq_len, k_out, v_out, k_scale_out, v_scale_out,
+                 weight_out, len_out, workspace)
+    with _on(k):
+        if workspace is None:
+            workspace = _scratch(kv8_evict_workspace_size(B, Hkv, cap, budget), k.device)
+        _check(lib().thrift_kv8_evict(B, Hkv, d, blk, cap, *st, _ptr(k), _ptr(v), _ptr(k_scale),
+                                      _ptr(v_scale), _ptr(weight), _ptr(seq_len), budget, sink,
+                                      recent, cap_o, *sto, _ptr(k_out), _ptr(v_out),
+                                      _ptr(k_scale_out), _ptr(v_scale_out), _ptr(weight_out),
+                                      _ptr(len_out), _ptr(workspace), workspace.numel(),
+                                      _stream(k)), "thrift_kv8_evict")
+
+
+class KV8Cache:
+    """An 8-bit KV cache of ``B`` sequences: codes, block scales, the weight
+    each token has received, and the cached lengths, all on the device."""
+
+    def __init__(self, B, Hkv, capacity, d=128, blk=64, dtype=torch.bfloat16, device="cuda"):
+        if B < 1 or Hkv < 1 or capacity < 1:
+            raise ThriftError("KV8Cache: B, Hkv and capacity must be positive")
+        self.blk, self.dtype = blk, dtype
+        shape = (B, Hkv, capacity, d)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(_F8)
+                          for _ in range(2))
+        self.k_scale, self.v_scale = (torch.zeros((B, Hkv, -(-capacity // blk)), device=device)
+                                      for _ in range(2))
+        self.weight = torch.zeros(shape[:3], device=device)
+        self.lengths = torch.zeros(B, dtype=torch.int32, device=device)
+        _kv8_cache(self.k, self.v, self.k_scale, self.v_scale, blk)
+
+    @property
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+    def append(self, k_new, v_new, n_new=None):
+        """k_new, v_new [B, T, Hkv, d]; n_new int32 [B] (default: T each).
+        Advances ``lengths``."""
+        if k_new.dtype != self.dtype or v_new.dtype != self.dtype:
+            raise ThriftError(f"k_new, v_new must be {self.dtype}")
+        thrift_kv8_append(k_new, v_new, *self.tensors, self.lengths, n_new, blk=self.blk,
+                          weight=self.weight, new_len=self.lengths)
+
+    def decode(self, q, scale=None, accumulate=False, out=None, lse=None, workspace=None):
+        """q [B,H,d] -> (out [B,H,d], lse f32 [B,H]); ``accumulate`` adds the
+        step's probabilities to ``weight``."""
+        if q.dtype != self.dtype:
+            raise ThriftError(f"q has dtype {q.dtype}, the cache holds {self.dtype}")
+        return thrift_kv8_decode(q, *self.tensors, self.lengths, blk=self.blk, scale=scale,
+                                 weight=self.weight if accumulate else None, out=out, lse=lse,
+                                 workspace=workspace)
+
+    def evict(self, budget, recent=0, sink=0, out=None, workspace=None):
+        """Cuts every sequence to ``budget`` tokens into ``out`` (another
+        KV8Cache of the same shape; one spare serves every layer in turn) and
+        returns it; without it, into a new cache."""
+        if out is None:
+            B, Hkv, cap, d = self.k.shape
+            out = KV8Cache(B, Hkv, cap, d, self.blk, self.dtype, self.k.device)
+        if out.blk != self.blk or out.dtype != self.dtype:
+            raise ThriftError("the two caches must agree in blk and dtype")
+        thrift_kv8_evict(*self.tensors, self.weight, self.lengths, budget, *out.tensors,
+                         out.weight, out.lengths, blk=self.blk, recent=recent, sink=sink,
+                         workspace=workspace)
+        return out
+
+
+# ----------------------------------------------------------------- linear --
+
+def nvfp4_linear_workspace_size(M, N, K) -> int:
+    return int(lib().nvfp4_linear_workspace_size(M, N, K))
+
+
+def nvfp4_linear(x, codes, scales, tensor_scale, out=None, workspace=None):
+    """y = x W^T: x [M, K] fp16/bf16 (M <= 64) and NVFP4 weights W [N, K] as
+    nvfp4_quantize leaves them (codes u8 [N, K/2], scales u8 [N, K/16],
+    tensor_scale f32 [1]) -> [M, N] in x's dtype.  K % 32 == 0."""
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ThriftError("x must be [M, K] and codes [N, K/2]")
+    M, K = x.shape
+    N = codes.shape[0]
+    dt = _dt(x)
+    _check_like(codes, (N, K // 2), torch.uint8, "codes")
+    _check_like(scales, (N, K // 16), torch.uint8, "scales")
+    _check_like(out, (M, N), x.dtype, "out")
+    if tensor_scale.dtype != torch.float32 or tensor_scale.numel() < 1:
+        raise ThriftError("tensor_scale must be float32 with at least one element")
+    if M > 64 or K == 0 or K % 32:
+        raise ThriftError("nvfp4_linear supports at most 64 rows and K a multiple of 32")
+    _same_device(x, codes, scales, tensor_scale, out, workspace)
+    _need_cuda(x, codes, scales, *(t for t in (out, workspace) if t is not None))
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    if M == 0 or N == 0:
+        return out
+    with _on(x):
+        if workspace is None:
+            workspace = _scratch(nvfp4_linear_workspace_size(M, N, K), x.device)
+        _check(lib().nvfp4_linear(_ptr(x), dt, M, N, K, _ptr(codes), _ptr(scales),
+                                  _ptr(tensor_scale), _ptr(out), _ptr(workspace),
+                                  workspace.numel(), _stream(x)), "nvfp4_linear")
+    return out
 
 
 # --------------------------------------------------------------- Attn-QAT --

@@ -337,6 +337,98 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
                                  void* out, float* lse, void* workspace, size_t ws_bytes,
                                  void* stream);
 
+/* ---------------------------------------------------------- 8-bit cache --
+ * A KV cache of one byte per value, beside the double cache above: decode
+ * over it reads half the bytes of a 16-bit cache, and it can be cut back to
+ * a budget of tokens.  The cache is plain caller-owned device memory:
+ *   k, v            E4M3 codes [B, Hkv, capacity, d], the d codes of a row
+ *                   contiguous, the other axes in any order: stride_b,
+ *                   stride_h, stride_t in bytes (multiples of 16, rows not
+ *                   overlapping; the stride of an axis of size 1 is not
+ *                   read).  K and V have the same strides, 16-byte aligned.
+ *   k_scale, v_scale  fp32 [B, Hkv, ceil(capacity / blk)]: one scale per block
+ *                   of blk tokens; a code stands for e4m3(code) * scale.
+ *   weight          fp32 [B, Hkv, capacity]: the attention weight each token
+ *                   has received so far (optional but for the eviction).
+ * Nothing has to be cleared: rows, scales and weights at or behind a
+ * sequence's length are never read.  Supported: d in {64, 128}, blk in {16,
+ * 32, 64, 128} (else THRIFT_ERR_UNSUPPORTED), H % Hkv == 0, either 16-bit
+ * type.  Lengths (int32 [B] on the device) are clamped to [0, capacity].
+ *
+ * Scales are powers of two: a block's is the smallest 2^e, e >= -120, with
+ * max|x| <= 448 * 2^e over the finite values that entered it; a code is x /
+ * scale rounded to nearest even.  A value that is not finite is stored as
+ * NaN and does not count for the scale.
+ *
+ * thrift_kv8_append: appends n_new[b] tokens (clamped to [0, max_new]; n_new
+ * NULL: max_new each) behind cache_len[b]: k_new, v_new 16-bit [B, max_new,
+ * Hkv, d] contiguous (token i of sequence b at [b, i]).  Tokens that would
+ * land at or past capacity are dropped.  A block whose scale grows has the
+ * codes it held re-encoded under the new scale (exact unless a value falls
+ * below 2^-6 of it).  weight (or NULL): zeroed for the new tokens.  new_len
+ * (or NULL): int32 [B] receives min(capacity, length + tokens appended); it
+ * may be cache_len itself, else must not overlap it.
+ *
+ * thrift_kv8_decode: q 16-bit [B, H, d]; per (sequence, head) the softmax of
+ * scale * (q . k_t) over the seq_len[b] cached tokens, applied to v.
+ *   out 16-bit [B, H, d] out;  lse fp32 [B, H] out (natural log; an empty
+ *   sequence gives a zero row and -inf);  weight (or NULL): += the sum over
+ *   the query heads of each kv head of the probability of each token.
+ *   A NaN among a row's inputs makes that row NaN.
+ *
+ * thrift_kv8_evict: writes into another cache (out_*, its own capacity >=
+ * min(budget, capacity), strides, and every tensor apart from the input's)
+ * what stays of each (sequence, kv head) when its tokens are cut to budget:
+ * all when there are no more than that; else the first sink, the last recent
+ * and, of the others, those of largest weight (ties to the earlier token; a
+ * NaN counts as -inf), in their order, with their weights.  Blocks are encoded
+ * anew from the values the codes stand for, as an append of those values to
+ * an empty cache would.  len_out int32 [B] = min(length, budget); rows behind
+ * it and their blocks keep what they held.  sink + recent <= budget.
+ *
+ * Workspaces: *_workspace_size bytes, 16-byte aligned, no initial content;
+ * calls that overlap on the GPU must not share one. */
+thrift_status thrift_kv8_append(const void* k_new, const void* v_new, thrift_dtype dt, int B,
+                                int Hkv, int d, int blk, int capacity, int64_t stride_b,
+                                int64_t stride_h, int64_t stride_t, const int32_t* cache_len,
+                                const int32_t* n_new, int max_new, void* k, void* v,
+                                float* k_scale, float* v_scale, float* weight, int32_t* new_len,
+                                void* stream);
+size_t thrift_kv8_decode_workspace_size(int B, int H, int Hkv, int capacity, int d,
+                                        int accumulate);
+thrift_status thrift_kv8_decode(const void* q, thrift_dtype dt, int B, int H, int Hkv, int d,
+                                int blk, int capacity, int64_t stride_b, int64_t stride_h,
+                                int64_t stride_t, const void* k, const void* v,
+                                const float* k_scale, const float* v_scale,
+                                const int32_t* seq_len, float scale, float* weight, void* out,
+                                float* lse, void* workspace, size_t ws_bytes, void* stream);
+size_t thrift_kv8_evict_workspace_size(int B, int Hkv, int capacity, int budget);
+thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int64_t stride_b,
+                               int64_t stride_h, int64_t stride_t, const void* k, const void* v,
+                               const float* k_scale, const float* v_scale, const float* weight,
+                               const int32_t* seq_len, int budget, int sink, int recent,
+                               int out_capacity, int64_t out_stride_b, int64_t out_stride_h,
+                               int64_t out_stride_t, void* k_out, void* v_out, float* k_scale_out,
+                               float* v_scale_out, float* weight_out, int32_t* len_out,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------- linear --
+ * y = x W^T for the few rows of a generation step and NVFP4 weights as
+ * nvfp4_quantize leaves them (blocks along the contraction): x 16-bit [M, K],
+ * codes [N, K/2], scales [N, K/16], tensor_scale one float on the device;
+ * out 16-bit [M, N] in x's type.  nvfp4_quantize takes at most 4096 columns;
+ * wider weights are quantised as [N * K / c, c] for a c that divides K (the
+ * same bytes).  A row of x holding a value that is not finite gives NaN.
+ * Requirements: 0 <= M <= 64 and K % 32 == 0 (else THRIFT_ERR_UNSUPPORTED),
+ * all pointers 16-byte aligned, contiguous.  Workspace:
+ * nvfp4_linear_workspace_size bytes, no initial content; calls that overlap
+ * on the GPU must not share one. */
+size_t nvfp4_linear_workspace_size(int M, int64_t N, int K);
+thrift_status nvfp4_linear(const void* x, thrift_dtype dt, int M, int64_t N, int K,
+                           const uint8_t* codes, const uint8_t* scales,
+                           const float* tensor_scale, void* out, void* workspace, size_t ws_bytes,
+                           void* stream);
+
 /* ------------------------------------------------------------ Attn-QAT --
  * "Attn-QAT: 4-Bit Attention With Quantization-Aware Training",
  * Metodologia: attention trained through a fake-quantised NVFP4 forward.
