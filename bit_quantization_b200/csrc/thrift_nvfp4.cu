@@ -698,6 +698,82 @@ thrift_status kv8_decode_impl(const void* q, const Kv8Geom& g, int H, const void
   return launch_status();
 }
 
+// --------------------------------------------------------------- linear --
+
+// cuTensorMapEncodeTiled, from the driver that is loaded (the library links
+// the runtime only).
+PFN_encode_tiled encode_tiled() {
+  static std::atomic<PFN_encode_tiled> fn{nullptr};
+  PFN_encode_tiled f = fn.load();
+  if (!f) {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &sym, cudaEnableDefault, &found) !=
+            cudaSuccess || found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = reinterpret_cast<PFN_encode_tiled>(sym);
+    fn.store(f);
+  }
+  return f;
+}
+
+int lin_rows(int M) { return M <= 2 ? 2 : M <= 5 ? 5 : M <= 8 ? 8 : kLinGroup; }
+
+// Workspace of a call, and where its parts are.
+size_t lin_workspace(int M, int K, int64_t* img, int64_t* part) {
+  const int rows = lin_rows(M);
+  *img = kLinOffImg;
+  *part = *img + ceil_div(M, kLinGroup) * ceil_div(K, kLinChunk) * (int64_t)lin_img(lin_cols(rows));
+  return (size_t)(*part + (int64_t)kLinMaxCtas * 2 * rows * 128 * 4);
+}
+
+template <int DT, int ROWS>
+thrift_status linear_launch(const LinParams& p, const uint8_t* codes, cudaStream_t st) {
+  using L = LinLayout<ROWS>;
+  static DeviceSet smem_done;
+  const auto encode = encode_tiled();
+  const auto kernel = linear_kernel<DT, ROWS>;
+  if (!encode || !smem_attr(kernel, L::SMEM, smem_done)) return THRIFT_ERR_CUDA;
+  CUtensorMap map;
+  const cuuint64_t dim[2] = {(cuuint64_t)p.K / 2, (cuuint64_t)p.N}, stride[1] = {dim[0]};
+  const cuuint32_t box[2] = {kLinChunk / 2, 128}, one[2] = {1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dim, stride, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return THRIFT_ERR_CUDA;
+  int cl = 1;  // CTAs that share a row of x: 2048 values each
+  while (cl < 8 && cl * 2048 < p.K) cl *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.M * cl);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)cl, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = cl > 1;
+  if (cudaLaunchKernelEx(&cfg, lin_digits_kernel<DT>, p, cl) != cudaSuccess) return THRIFT_ERR_CUDA;
+  const int64_t units = ceil_div(p.M, kLinGroup) * ceil_div(p.N, 128) * p.chunks;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, std::min(sm_count(), kLinMaxCtas)));
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = L::SMEM;
+  at[0] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, map, p) == cudaSuccess ? THRIFT_OK : THRIFT_ERR_CUDA;
+}
+
+template <int DT>
+thrift_status linear_dispatch(const LinParams& p, const uint8_t* codes, cudaStream_t st) {
+  switch (lin_rows(p.M)) {
+    case 2: return linear_launch<DT, 2>(p, codes, st);
+    case 5: return linear_launch<DT, 5>(p, codes, st);
+    case 8: return linear_launch<DT, 8>(p, codes, st);
+    default: return linear_launch<DT, kLinGroup>(p, codes, st);
+  }
+}
+
 // Failure-detection aid: one thread waits, with the library's own bounded
 // waits, on something that never completes: an mbarrier that nothing arrives
 // on (mode 0) or a global word that nothing writes (mode 1).  The wait gives
@@ -1478,8 +1554,9 @@ thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int
 // -------------------------------------------------------------- linear --
 
 size_t nvfp4_linear_workspace_size(int M, int64_t N, int K) {
-  if (M <= 0 || M > kLinMaxM || N <= 0 || K <= 0 || K % 32) return 0;
-  return 256;
+  if (M <= 0 || M > kLinMaxM || N <= 0 || K <= 0 || K % 32 || K > kLinMaxK) return 0;
+  int64_t img, part;
+  return lin_workspace(M, K, &img, &part);
 }
 
 thrift_status nvfp4_linear(const void* x, thrift_dtype dt, int M, int64_t N, int K,
@@ -1488,19 +1565,26 @@ thrift_status nvfp4_linear(const void* x, thrift_dtype dt, int M, int64_t N, int
                            void* stream) {
   if (dt != THRIFT_F16 && dt != THRIFT_BF16) return THRIFT_ERR_ARG;
   if (M < 0 || N < 0 || K <= 0 || K % 16) return THRIFT_ERR_ARG;
-  if (M > kLinMaxM || K % 32 || N > (1 << 30) || K > (1 << 24)) return THRIFT_ERR_UNSUPPORTED;
+  if (M > kLinMaxM || K % 32 || K > kLinMaxK || N > (1 << 30)) return THRIFT_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return THRIFT_OK;
   if (!x || !codes || !scales || !tensor_scale || !out || !workspace) return THRIFT_ERR_ARG;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(out) ||
       !aligned16(workspace))
     return THRIFT_ERR_ARG;
-  if (ws_bytes < nvfp4_linear_workspace_size(M, N, K)) return THRIFT_ERR_ARG;
+  LinParams p = {};
+  if (ws_bytes < lin_workspace(M, K, &p.img, &p.part)) return THRIFT_ERR_ARG;
+  p.x = static_cast<const uint16_t*>(x);
+  p.scales = scales;
+  p.gs = tensor_scale;
+  p.y = static_cast<uint16_t*>(out);
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.M = M;
+  p.K = K;
+  p.N = (int)N;
+  p.cols = lin_cols(lin_rows(M));
+  p.chunks = (int)ceil_div(K, kLinChunk);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)ceil_div(N, 8);
-  const auto kernel = dt == THRIFT_BF16 ? linear_kernel<1> : linear_kernel<0>;
-  kernel<<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x), M, K, (int)N, codes, scales,
-                               tensor_scale, static_cast<uint16_t*>(out));
-  return launch_status();
+  return dt == THRIFT_BF16 ? linear_dispatch<1>(p, codes, st) : linear_dispatch<0>(p, codes, st);
 }
 
 }  // extern "C"

@@ -130,9 +130,9 @@ def lib():
         L.thrift_kv8_evict.argtypes = [i32, i32, i32, i32, i32, i64, i64, i64, P, P, P, P, P, P,
                                        i32, i32, i32, i32, i64, i64, i64, P, P, P, P, P, P, P, sz,
                                        P]
+        L.nvfp4_linear.restype = i32
         L.nvfp4_linear_workspace_size.restype = sz
         L.nvfp4_linear_workspace_size.argtypes = [i32, i64, i32]
-        L.nvfp4_linear.restype = i32
         L.nvfp4_linear.argtypes = [P, i32, i32, i64, i32, P, P, P, P, P, sz, P]
         _lib = L
     return _lib
@@ -828,8 +828,9 @@ def nvfp4_linear(x, codes, scales, tensor_scale, out=None, workspace=None):
     _check_like(out, (M, N), x.dtype, "out")
     if tensor_scale.dtype != torch.float32 or tensor_scale.numel() < 1:
         raise ThriftError("tensor_scale must be float32 with at least one element")
-    if M > 64 or K == 0 or K % 32:
-        raise ThriftError("nvfp4_linear supports at most 64 rows and K a multiple of 32")
+    if M > 64 or K == 0 or K % 32 or K > 1 << 19:
+        raise ThriftError("nvfp4_linear supports at most 64 rows and K a multiple of 32 up to "
+                          "524288")
     _same_device(x, codes, scales, tensor_scale, out, workspace)
     _need_cuda(x, codes, scales, *(t for t in (out, workspace) if t is not None))
     if out is None:

@@ -419,10 +419,10 @@ thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int
  * out 16-bit [M, N] in x's type.  nvfp4_quantize takes at most 4096 columns;
  * wider weights are quantised as [N * K / c, c] for a c that divides K (the
  * same bytes).  A row of x holding a value that is not finite gives NaN.
- * Requirements: 0 <= M <= 64 and K % 32 == 0 (else THRIFT_ERR_UNSUPPORTED),
- * all pointers 16-byte aligned, contiguous.  Workspace:
- * nvfp4_linear_workspace_size bytes, no initial content; calls that overlap
- * on the GPU must not share one. */
+ * Requirements: 0 <= M <= 64, K % 32 == 0 and K <= 524288 (else
+ * THRIFT_ERR_UNSUPPORTED), all pointers 16-byte aligned, contiguous; out
+ * overlaps no input.  Workspace: nvfp4_linear_workspace_size bytes, no initial
+ * content; calls that overlap on the GPU must not share one. */
 size_t nvfp4_linear_workspace_size(int M, int64_t N, int K);
 thrift_status nvfp4_linear(const void* x, thrift_dtype dt, int M, int64_t N, int K,
                            const uint8_t* codes, const uint8_t* scales,

@@ -176,7 +176,7 @@ def test_linear_abi_refuses(L):
         (dict(dt=5), ops.ERR_ARG), (dict(M=-1), ops.ERR_ARG), (dict(K=24), ops.ERR_ARG),
         (dict(K=48), ops.ERR_UNSUPPORTED), (dict(M=65), ops.ERR_UNSUPPORTED),
         (dict(x=None), ops.ERR_ARG), (dict(c=P(8)), ops.ERR_ARG), (dict(g=None), ops.ERR_ARG),
-        (dict(wb=16), ops.ERR_ARG), (dict(M=0), ops.OK), (dict(N=0), ops.OK),
+        (dict(K=(1 << 19) + 32), ops.ERR_UNSUPPORTED), (dict(wb=16), ops.ERR_ARG), (dict(M=0), ops.OK), (dict(N=0), ops.OK),
     ):
         assert call(**kw) == want, kw
 
