@@ -39,6 +39,7 @@ constexpr int kLinGroup = 16;       // rows of x in one pass over the weights
 constexpr int kLinDigits = 6;
 constexpr int kLinChunk = 256;      // K of one stage: 128 bytes of codes a weight row
 constexpr int kLinMaxCtas = 256;    // one an SM
+constexpr int kLinDigitThreads = 512;  // 8 values of x each
 constexpr uint32_t kLinABytes = 128 * (kLinChunk / 2);  // codes of 128 weight rows
 constexpr uint32_t kLinSfBytes = (kLinChunk / 64) * 512;  // a scale-factor image
 
@@ -62,6 +63,21 @@ struct LinParams {
   int64_t part;
   int M, K, N;
   int cols, chunks;
+  int run, longer;  // units a CTA takes; the first `longer` of them one more
+};
+
+// A unit of work: chunk c of weight tile `tile` for group `grp` of rows of x.
+struct LinUnit {
+  int c, tile, grp;
+  __device__ __forceinline__ void next(int chunks, int ntiles) {
+    if (++c == chunks) {
+      c = 0;
+      if (++tile == ntiles) {
+        tile = 0;
+        ++grp;
+      }
+    }
+  }
 };
 
 // A byte of two E2M1 codes -> their values.
@@ -79,20 +95,22 @@ __device__ __forceinline__ float2 e2m1x2_decode(uint32_t c) {
 // One row of x: a cluster of CTAs finds its largest value, then every thread
 // writes the digits of 8 values, two threads the scale of a block of 16.
 template <int DT>
-__global__ void __launch_bounds__(256) lin_digits_kernel(const LinParams p, int cl) {
+__global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinParams p, int cl) {
   __shared__ uint32_t s_max;
   __shared__ float s_red;
   const int m = blockIdx.x / cl, rank = blockIdx.x % cl, tid = threadIdx.x;
   pdl_trigger();
   if (blockIdx.x == 0)
-    for (int i = tid; i < kLinMaxCtas * 4; i += 256) reinterpret_cast<uint32_t*>(p.ws)[i] = 0;
+    for (int i = tid; i < kLinMaxCtas * 4; i += kLinDigitThreads) reinterpret_cast<uint32_t*>(p.ws)[i] = 0;
   if (tid == 0) s_max = 0;
   __syncthreads();
   const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.K);
-  const int n8 = p.K / 8, first = rank * 256 + tid, step = cl * 256;
+  const int n8 = p.K / 8, first = rank * kLinDigitThreads + tid, step = cl * kLinDigitThreads;
   uint32_t a = 0;  // bits of |x|: ordered, infinities and NaN on top
+  uint4 v = make_uint4(0, 0, 0, 0), head = v;  // head: the first, kept for the digits
   for (int i = first; i < n8; i += step) {
-    const uint4 v = __ldg(src + i);
+    v = __ldg(src + i);
+    if (i == first) head = v;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) a = max(a, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
@@ -109,18 +127,18 @@ __global__ void __launch_bounds__(256) lin_digits_kernel(const LinParams p, int 
   const bool finite = a < (DT == 1 ? 0x7F80u : 0x7C00u);
   // the largest value to [2^9, 2^10), in two factors: 2^135 is not an fp32 number
   const float top = h2f<DT>((uint16_t)a);
-  const int E = top > 0.0f && finite ? ilogbf(top) : 0;
+  const int E = top > 0.0f && finite ? (int)(__float_as_uint(top) >> 23) - 127 : 0;
   const int e = 9 - E, e1 = e >> 1, e2 = e - e1;
   const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23);
   const float f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
   if (rank == 0 && tid == 0)
-    reinterpret_cast<float*>(p.ws + kLinOffUnit)[m] = finite ? ldexpf(1.0f, -e) : NAN;
+    reinterpret_cast<float*>(p.ws + kLinOffUnit)[m] = finite ? 1.0f / f1 / f2 : NAN;
   const int grp = m / kLinGroup, col = kLinDigits * (m % kLinGroup);
   uint8_t* img = p.ws + p.img + (int64_t)grp * p.chunks * lin_img(p.cols);
   // the last chunk is written to its end: its weights are zeros there, x too
   for (int i = first; i < p.chunks * (kLinChunk / 8); i += step) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (i < n8 && finite) v = __ldg(src + i);
+    v = make_uint4(0, 0, 0, 0);
+    if (i < n8 && finite) v = i == first ? head : __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float x[8], top8 = 0.0f;
 #pragma unroll
@@ -219,41 +237,48 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  const int chunks = p.chunks, ntiles = (int)ceil_div(p.N, 128);
-  const int64_t units = ceil_div(p.M, kLinGroup) * ntiles * chunks;
-  const int P = gridDim.x, cta = blockIdx.x;
-  const int64_t u0 = units * cta / P;
-  const int n = (int)(units * (cta + 1) / P - u0);
-  const int64_t t0 = u0 / chunks;  // first (group, tile)
-  const int c0 = (int)(u0 % chunks);
+  const int chunks = p.chunks, ntiles = (int)ceil_div(p.N, 128), cta = blockIdx.x;
+  const int n = p.run + (cta < p.longer);
+  const int u0 = p.run * cta + min(cta, p.longer);
+  LinUnit u;
+  u.c = u0 % chunks;
+  u.tile = u0 / chunks % ntiles;
+  u.grp = u0 / chunks / ntiles;
 
   if (warp == 0) {
     if (lane == 0) {
-      auto codes = [&](int k) {
-        const int64_t t = t0 + (c0 + k) / chunks;
-        tma_load_2d(sm + (k % L::STAGES) * L::STAGE, &map, (c0 + k) % chunks * (kLinChunk / 2),
-                    (int)(t % ntiles) * 128, full + k % L::STAGES);
+      auto codes = [&](int sl, const LinUnit& q) {
+        tma_load_2d(sm + sl * L::STAGE, &map, q.c * (kLinChunk / 2), q.tile * 128, full + sl);
       };
-      auto digits = [&](int k) {
-        const int64_t t = t0 + (c0 + k) / chunks;
-        bulk_g2s(sm + (k % L::STAGES) * L::STAGE + L::B,
-                 p.ws + p.img + (t / ntiles * chunks + (c0 + k) % chunks) * lin_img(L::COLS),
-                 lin_img(L::COLS), full + k % L::STAGES);
+      auto digits = [&](int sl, const LinUnit& q) {
+        bulk_g2s(sm + sl * L::STAGE + L::B,
+                 p.ws + p.img + ((int64_t)q.grp * chunks + q.c) * lin_img(L::COLS),
+                 lin_img(L::COLS), full + sl);
       };
       const int ahead = min(n, L::STAGES);
+      LinUnit q = u;
       for (int k = 0; k < ahead; ++k) {  // the weights do not wait for the digits
         mbar_arrive_expect_tx(full + k, kLinABytes + lin_img(L::COLS));
-        codes(k);
+        codes(k, q);
+        q.next(chunks, ntiles);
       }
       pdl_wait();
-      for (int k = 0; k < ahead; ++k) digits(k);
-      int k = ahead;
+      for (int k = 0; k < ahead; ++k) {
+        digits(k, u);
+        u.next(chunks, ntiles);
+      }
+      int k = ahead, sl = 0, par = 0;
       for (; k < n; ++k) {
-        const int sl = k % L::STAGES;
-        if (!mbar_wait(empty + sl, (k / L::STAGES - 1) & 1, s_abort)) break;
+        if (sl == L::STAGES) {
+          sl = 0;
+          par ^= 1;
+        }
+        if (!mbar_wait(empty + sl, par, s_abort)) break;
         mbar_arrive_expect_tx(full + sl, kLinABytes + lin_img(L::COLS));
-        codes(k);
-        digits(k);
+        codes(sl, u);
+        digits(sl, u);
+        u.next(chunks, ntiles);
+        ++sl;
       }
       // every copy has landed before the CTA ends
       int dummy = 0;
@@ -266,14 +291,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     const uint64_t d_sf = make_sdesc(base, 512, 128, SW_NONE);
     const uint64_t d_ab = make_sdesc(base, 16, 1024, SW_128B);
     constexpr uint32_t id = idesc_nvf4(128, L::COLS);
-    int seg = 0;
+    int seg = 0, sl = 0, par = 0, c = u.c;
     for (int k = 0; k < n; ++k) {
-      const int sl = k % L::STAGES, c = (c0 + k) % chunks;
       const bool first = k == 0 || c == 0, last = k + 1 == n || c + 1 == chunks;
       if (first && seg >= 2 &&
           !__all_sync(0xffffffffu, mbar_wait(sum_empty + (seg & 1), ((seg >> 1) - 1) & 1, s_abort)))
         break;
-      if (!__all_sync(0xffffffffu, mbar_wait(full + sl, (k / L::STAGES) & 1, s_abort))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(full + sl, par, s_abort))) break;
       tc_fence_after();
       if (leader) {
         const uint32_t stg = sl * L::STAGE, sf = tmem + L::T_SF + 32 * (k & 1);
@@ -292,17 +316,23 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
       }
       __syncwarp();
       seg += last;
+      c = c + 1 == chunks ? 0 : c + 1;
+      if (++sl == L::STAGES) {
+        sl = 0;
+        par ^= 1;
+      }
     }
   } else if (warp < kLinEpiWarp) {
     // ------------------------------------------------- weights' scales --
     const int row = tid - 32 * kLinSfWarp;
     const int64_t lds = p.K / 16;
     const bool whole = p.K % kLinChunk == 0;  // 16 aligned bytes a row and chunk
-    auto load = [&](int k) {
+    auto load = [&](int k) {  // units in order
       uint4 v = make_uint4(0, 0, 0, 0);
       if (k >= n) return v;
-      const int64_t r = (t0 + (c0 + k) / chunks) % ntiles * 128 + row;
-      const int c = (c0 + k) % chunks;
+      const int64_t r = u.tile * 128 + row;
+      const int c = u.c;
+      u.next(chunks, ntiles);
       if (r >= p.N) return v;
       const uint8_t* s = p.scales + r * lds + c * 16;
       if (whole) return __ldg(reinterpret_cast<const uint4*>(s));
@@ -318,15 +348,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) ring[i] = load(i);
     bool ok = true;
+    int sl = 0, par = 1;  // of the stage's previous use; none in the first round
     for (int k0 = 0; k0 < n && ok; k0 += AHEAD) {
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        const int k = k0 + i, sl = k % L::STAGES;
+        const int k = k0 + i;
         if (k >= n || !ok) continue;
         const uint4 v = ring[i];
         ring[i] = load(k + AHEAD);
         if (k >= L::STAGES)
-          ok = __all_sync(0xffffffffu, mbar_wait(empty + sl, (k / L::STAGES - 1) & 1, s_abort));
+          ok = __all_sync(0xffffffffu, mbar_wait(empty + sl, par, s_abort));
         if (!ok) continue;
         uint32_t* to = reinterpret_cast<uint32_t*>(sm + sl * L::STAGE + L::SFA + sf_offset(row, 0));
         to[0] = v.x;
@@ -336,10 +367,18 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full + sl);
+        if (++sl == L::STAGES) {
+          sl = 0;
+          par ^= 1;
+        }
       }
     }
   } else {
     // ------------------------------------------------------------- sums --
+    auto owner = [&](int unit) {
+      const int lead = p.longer * (p.run + 1);
+      return unit < lead ? unit / (p.run + 1) : p.longer + (unit - lead) / p.run;
+    };
     pdl_wait();
     const int quarter = warp & 3, row = 32 * quarter + lane;
     const float g = __ldg(p.gs);
@@ -348,13 +387,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
     float* part = reinterpret_cast<float*>(p.ws + p.part) + row;
     int seg = 0;
     for (int k = 0; k < n; ++seg) {
-      const int c = (c0 + k) % chunks, len = min(n - k, chunks - c);
-      const int64_t t = t0 + (c0 + k) / chunks;
-      const int grp = (int)(t / ntiles);
-      const int64_t w = t % ntiles * 128 + row;
+      const int len = min(n - k, chunks - u.c), grp = u.grp, t = grp * ntiles + u.tile;
+      const int64_t w = (int64_t)u.tile * 128 + row;
       const int M = min(kLinGroup, p.M - grp * kLinGroup);
       uint16_t* y = p.y + (int64_t)grp * kLinGroup * p.N + w;
       k += len;
+      u.c = chunks - 1;
+      u.next(chunks, ntiles);
       if (!__all_sync(0xffffffffu, mbar_wait(sum_full + (seg & 1), (seg >> 1) & 1, s_abort))) break;
       tc_fence_after();
       float acc[L::COLS];
@@ -373,9 +412,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
       }
       if (len < chunks) {
         // a shared tile: CTAs a .. b have a part of it
-        const int64_t first = t * chunks;
-        const int a = (int)(((first + 1) * P - 1) / units);
-        const int b = (int)(((first + chunks) * P - 1) / units);
+        const int first = t * chunks, a = owner(first), b = owner(first + chunks - 1);
+        const bool second = p.run * a + min(a, p.longer) < first;  // not a's first tile
         float* mine = part + (int64_t)(2 * cta + (seg > 0)) * ROWS * 128;
 #pragma unroll
         for (int m = 0; m < ROWS; ++m)
@@ -386,14 +424,25 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         if (lane == 0) before = atomicAdd(arrived + 4 * a + quarter, 1u);
         if (__shfl_sync(0xffffffffu, before, 0) != (uint32_t)(b - a)) continue;
         __threadfence();
+        // in the order of the CTAs, the loads of BATCH of them together
+        constexpr int BATCH = 16 / ROWS;
+        const float* theirs = part + (int64_t)2 * a * ROWS * 128;
 #pragma unroll
-        for (int m = 0; m < ROWS; ++m) v[m] = 0.0f;
-        for (int i = a; i <= b; ++i) {
-          const int second = units * i / P < first;  // this tile is not its first
-          const float* theirs = part + (int64_t)(2 * i + second) * ROWS * 128;
+        for (int m = 0; m < ROWS; ++m)
+          v[m] = m < M ? __ldcg(theirs + (second * ROWS + m) * 128) : 0.0f;
+        for (int i = 1; i <= b - a; i += BATCH) {
+          float got[BATCH][ROWS];
 #pragma unroll
-          for (int m = 0; m < ROWS; ++m)
-            if (m < M) v[m] += __ldcg(theirs + m * 128);
+          for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m)
+              got[j][m] = i + j <= b - a && m < M
+                              ? __ldcg(theirs + (int64_t)(2 * (i + j) * ROWS + m) * 128)
+                              : 0.0f;
+#pragma unroll
+          for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) v[m] += got[j][m];
         }
       }
       if (w < p.N) {

@@ -728,7 +728,12 @@ size_t lin_workspace(int M, int K, int64_t* img, int64_t* part) {
 }
 
 template <int DT, int ROWS>
-thrift_status linear_launch(const LinParams& p, const uint8_t* codes, cudaStream_t st) {
+thrift_status linear_launch(LinParams p, const uint8_t* codes, cudaStream_t st) {
+  const int64_t units = ceil_div(p.M, kLinGroup) * ceil_div(p.N, 128) * p.chunks;
+  if (units > 1 << 30) return THRIFT_ERR_UNSUPPORTED;
+  const int grid = (int)std::min<int64_t>(units, std::min(sm_count(), kLinMaxCtas));
+  p.run = (int)(units / grid);
+  p.longer = (int)(units % grid);
   using L = LinLayout<ROWS>;
   static DeviceSet smem_done;
   const auto encode = encode_tiled();
@@ -741,11 +746,11 @@ thrift_status linear_launch(const LinParams& p, const uint8_t* codes, cudaStream
              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return THRIFT_ERR_CUDA;
-  int cl = 1;  // CTAs that share a row of x: 2048 values each
-  while (cl < 8 && cl * 2048 < p.K) cl *= 2;
+  int cl = 1;  // CTAs that share a row of x, 8 values a thread
+  while (cl < 8 && cl * 8 * kLinDigitThreads < p.K) cl *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.M * cl);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kLinDigitThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -753,8 +758,7 @@ thrift_status linear_launch(const LinParams& p, const uint8_t* codes, cudaStream
   cfg.attrs = at;
   cfg.numAttrs = cl > 1;
   if (cudaLaunchKernelEx(&cfg, lin_digits_kernel<DT>, p, cl) != cudaSuccess) return THRIFT_ERR_CUDA;
-  const int64_t units = ceil_div(p.M, kLinGroup) * ceil_div(p.N, 128) * p.chunks;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, std::min(sm_count(), kLinMaxCtas)));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = L::SMEM;
   at[0] = {};
