@@ -44,6 +44,13 @@ __device__ __forceinline__ float2 e4m3x2_decode(uint32_t c) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// 2^x, to two units in the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; }
 
 // Eight values -> eight codes under 1 / scale; what is not finite becomes NaN.
@@ -193,99 +200,534 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
 }
 
 // ----------------------------------------------------------------- decode --
+//
+// One new query token per sequence attends to its cached tokens: per (kv head,
+// sequence) the 256 (d = 128) bytes of a token are read once for all G query
+// heads of the group, which bounds the kernel (4 G d products a token are
+// 0.3 of the tensor cores' time at G = 16, far less below).  So the kernel is
+// built to keep loads in flight: every warp streams its own tokens from memory
+// to registers, 32 (d = 64: 64) at a time, the next ones' keys while the
+// values of these are used and the other way round; nothing is staged, no warp
+// waits for another before its tokens are done.
+//
+//   S^T [16 tokens, 8 heads] = K Q^T, O^T [16 channels, 8 heads] += V^T P^T
+//
+// run on register products (16 x 8 x 16, fp32 sums) whose operands are the
+// registers that were loaded: K's codes become exact fp16 pairs in one
+// instruction, V's after the bytes of two tokens are laced (the d axis of S
+// and the channel of O are numbered as the loads leave them), and P^T is the
+// transpose of the probabilities as S^T leaves them.  q enters as fp16, bf16
+// brought there by a power of two of the row's largest value (an element
+// 2^-28 below it and less keeps an error of 2^-39 of it).  A probability
+// enters as fp16, relative to the running maximum; sums of it are fp32.  O is
+// kept in units of the scale of the V block at hand, and moves to another
+// block's by an exact power of two.
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kKv8DecWarps = 4, kKv8DecCtas = 3;  // 168 registers a thread
+constexpr int kKv8MaxCtas = 512;
+constexpr int kKv8HeadGroup = 16;                 // query heads in one pass over the cache
 
-// Scores of one key (d codes at kp, 16-byte aligned) with a query row in
-// shared memory.
+// Tokens a warp takes at a time, and a CTA.
+__host__ __device__ constexpr int kv8_step(int d) { return 4096 / d; }
+__host__ __device__ constexpr int kv8_unit(int d) { return kKv8DecWarps * kv8_step(d); }
+
+struct Kv8Dec {
+  Kv8Geom g;
+  int H, G, HG, Gc;  // query heads, a group's, its parts of at most 16, a part's
+  const uint16_t* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* ks;
+  const float* vs;
+  const int32_t* len;
+  float scale;      // log2 e times the softmax scale
+  float* part_o;    // [CTA][2][Gc][d], relative to the part's own maximum
+  float* part_ml;   // [CTA][2][Gc][2] (maximum in log2 units, sum)
+  float* norm;      // [B, H, 2] (maximum, 1 / sum), or NULL
+  float* scores;    // [B, Hkv, HG, capacity, Gc rounded to even] (log2 units), or NULL
+  float* weight;
+  uint16_t* out;
+  float* lse;
+  int ctas;
+};
+
+// The work of a step is a row of units (sequence, kv head, part of the group,
+// kv8_unit tokens), dealt to the CTAs in equal runs whatever the lengths are.
+struct Kv8Plan {
+  int total, run, longer;  // the first `longer` CTAs take run + 1 units, the others run
+  __device__ __forceinline__ void set(int units, int ctas) {
+    total = units;
+    run = units / ctas;
+    longer = units % ctas;
+  }
+  __device__ __forceinline__ int first(int cta) const { return run * cta + min(cta, longer); }
+  __device__ __forceinline__ int owner(int unit) const {
+    const int lead = longer * (run + 1);
+    return unit < lead ? unit / (run + 1) : longer + (unit - lead) / run;
+  }
+};
+
+// Units of all sequences, and of those before sequence `upto`, by a whole CTA
+// (tmp: 2 ints a warp).
 template <int D>
-__device__ __forceinline__ float kv8_dot(const uint8_t* kp, const float* qs) {
-  float acc = 0.0f;
-#pragma unroll
-  for (int c = 0; c < D; c += 16) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(kp + c));
-    float x[8];
-    kv8_decode8(make_uint2(w.x, w.y), x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc = fmaf(x[i], qs[c + i], acc);
-    kv8_decode8(make_uint2(w.z, w.w), x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc = fmaf(x[i], qs[c + 8 + i], acc);
+__device__ __forceinline__ int2 kv8_count(const Kv8Dec& p, int upto, int* tmp) {
+  int all = 0, before = 0;
+  for (int b = threadIdx.x; b < p.g.B; b += blockDim.x) {
+    const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
+    all += n;
+    if (b < upto) before += n;
   }
-  return acc;
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    tmp[2 * (threadIdx.x >> 5)] = all;
+    tmp[2 * (threadIdx.x >> 5) + 1] = before;
+  }
+  __syncthreads();
+  all = before = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+    all += tmp[2 * w];
+    before += tmp[2 * w + 1];
+  }
+  const int per = p.g.Hkv * p.HG;
+  return make_int2(all * per, before * per);
 }
 
-// One CTA per (query head, sequence): 128 keys at a time, one per thread,
-// one running maximum and sum; then one channel per thread.
-template <int DT, int D>
-__global__ void __launch_bounds__(128) kv8_decode_kernel(
-    const uint16_t* __restrict__ q, Kv8Geom g, int H, const uint8_t* __restrict__ k,
-    const uint8_t* __restrict__ v, const float* __restrict__ ks, const float* __restrict__ vs,
-    const int32_t* __restrict__ seq_len, float scale, uint16_t* __restrict__ out,
-    float* __restrict__ lse) {
-  __shared__ float qs[D], ps[128], red[4];
-  const int hq = blockIdx.x, b = blockIdx.y, h = hq / (H / g.Hkv), tid = threadIdx.x;
-  const int len = g.len(seq_len, b);
-  const int64_t bh = (int64_t)b * H + hq;
-  if (tid < D) qs[tid] = h2f<DT>(__ldg(q + bh * D + tid));
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int t0 = 0; t0 < len; t0 += 128) {
-    __syncthreads();  // qs is in; ps of the previous keys has been read
-    const int t = t0 + tid;
-    float s = -INFINITY;
-    if (t < len)
-      s = kv8_dot<D>(k + g.row(b, h, t), qs) *
-          (__ldg(ks + g.scale(b, h, t / g.blk)) * scale * kLog2e);
-    float mx = s;
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    const float p = t < len ? exp2f(s - ref) : 0.0f;
-    const float alpha = exp2f(m - ref);
-    l = fmaf(l, alpha, p);
-    o *= alpha;
-    m = mx;
-    ps[tid] = t < len ? p * __ldg(vs + g.scale(b, h, t / g.blk)) : 0.0f;
-    __syncthreads();
-    if (tid < D)
-      for (int i = 0; i < min(128, len - t0); ++i)
-        o = fmaf(ps[i], e4m3x2_decode(__ldg(v + g.row(b, h, t0 + i) + tid)).x, o);
-  }
-#pragma unroll
-  for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = l;
-  __syncthreads();
-  l = red[0] + red[1] + red[2] + red[3];
-  if (tid < D) out[bh * D + tid] = f2h<DT>(len > 0 ? o / l : 0.0f);
-  if (tid == 0) lse[bh] = len > 0 ? m * kLn2 + logf(l) : -INFINITY;
+// Two E4M3 codes (the low or high half of c) -> two fp16 values (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 ldg_stream16(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint2 ldg_stream8(const uint8_t* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+               : "=r"(r.x), "=r"(r.y)
+               : "l"(p));
+  return r;
 }
 
-// weight[b, h, t] += sum over the group's heads of exp(s - lse).
-template <int DT, int D>
-__global__ void __launch_bounds__(128) kv8_weight_kernel(
-    const uint16_t* __restrict__ q, Kv8Geom g, int H, const uint8_t* __restrict__ k,
-    const float* __restrict__ ks, const int32_t* __restrict__ seq_len, float scale,
-    const float* __restrict__ lse, float* __restrict__ weight) {
-  __shared__ float qs[D];
-  const int h = blockIdx.y, b = blockIdx.z, G = H / g.Hkv, t = blockIdx.x * 128 + threadIdx.x;
-  const int len = g.len(seq_len, b);
-  if ((int)blockIdx.x * 128 >= len) return;
-  float sum = 0.0f;
-  for (int r = 0; r < G; ++r) {
-    const int64_t bh = (int64_t)b * H + h * G + r;
-    __syncthreads();
-    if (threadIdx.x < D) qs[threadIdx.x] = h2f<DT>(__ldg(q + bh * D + threadIdx.x));
-    __syncthreads();
-    if (t < len)
-      sum += expf(kv8_dot<D>(k + g.row(b, h, t), qs) *
-                      (__ldg(ks + g.scale(b, h, t / g.blk)) * scale) -
-                  __ldg(lse + bh));
+// NT: heads of a part in eights.
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
+    kv8_decode_kernel(const Kv8Dec p) {
+  constexpr int STEP = kv8_step(D), UNIT = kv8_unit(D), NG = STEP / 16;
+  constexpr int KS = D / 16;       // products along d
+  constexpr int VW = D / 32;       // words of a token's channels a thread holds
+  __shared__ float s_o[kKv8DecWarps][8 * NT][D + 1];
+  __shared__ float s_ml[kKv8DecWarps][8 * NT][2];
+  __shared__ float s_qs[8 * NT];
+  __shared__ __align__(16) uint16_t s_q[8 * NT][D];
+  __shared__ int tmp[2 * kKv8DecWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
+  const int Gp = (p.Gc + 1) & ~1;
+  pdl_trigger();
+  Kv8Plan plan;
+  plan.set(kv8_count<D>(p, 0, tmp).x, p.ctas);
+  int u = plan.first(blockIdx.x);
+  const int uend = plan.first(blockIdx.x + 1);
+  if (u >= uend) return;
+  // the sequence of unit u
+  const int per = p.g.Hkv * p.HG;
+  int b = 0, n = 0, rel = u;
+  for (int b0 = 0;; b0 += 32) {  // 32 sequences at a time
+    const int mine = b0 + lane < p.g.B ? (int)ceil_div(p.g.len(p.len, b0 + lane), UNIT) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, upto * per > rel);
+    const int at = past ? __ffs(past) - 1 : 31;
+    const int before = __shfl_sync(0xffffffffu, upto - mine, at);
+    n = __shfl_sync(0xffffffffu, mine, at);
+    if (past || b0 + 32 >= p.g.B) {
+      b = b0 + at;
+      rel -= before * per;
+      break;
+    }
+    rel -= (before + n) * per;
   }
-  if (t < len) weight[((int64_t)b * g.Hkv + h) * g.capacity + t] += sum;
+  int pair = rel / n, j = rel - pair * n;  // (kv head, part), unit of the sequence
+  for (int seg = 0; u < uend; ++seg) {
+    const int len = p.g.len(p.len, b), h = pair / p.HG, part = pair - h * p.HG;
+    const int jn = min(n - j, uend - u), heads = min(p.Gc, p.G - part * p.Gc);
+    const int64_t bh = (int64_t)b * p.H + h * p.G + part * p.Gc;  // first query head
+    // ---- q as fp16, two threads of a warp group a row
+    __syncthreads();
+    for (int r = warp; r < 8 * NT; r += kKv8DecWarps) {
+      float x[D / 32], top = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        x[i] = r < heads ? h2f<DT>(__ldg(p.q + (bh + r) * D + 32 * i + lane)) : 0.0f;
+        top = fmaxf(top, fabsf(x[i]));
+        bad |= !finite_f(x[i]);
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      float f = 1.0f, un = 1.0f;
+      if (DT == 1) {  // the largest value to [2^14, 2^15)
+        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23);
+        const int sh = min(max(141 - e, -126), 126);
+        f = __uint_as_float((uint32_t)(sh + 127) << 23);
+        un = __uint_as_float((uint32_t)(127 - sh) << 23);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        s_q[r][32 * i + lane] = __half_as_ushort(__float2half_rn(bad ? 0.0f : x[i] * f));
+      if (lane == 0) s_qs[r] = bad ? NAN : un * p.scale;
+    }
+    __syncthreads();
+    uint2 qf[NT][KS];
+    float qs[NT][2];
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        qf[a][s] = *reinterpret_cast<const uint2*>(
+            &s_q[8 * a + gr][64 * (s >> 2) + 16 * t + 4 * (s & 3)]);
+      qs[a][0] = s_qs[8 * a + 2 * t];
+      qs[a][1] = s_qs[8 * a + 2 * t + 1];
+    }
+    const uint8_t* kb = p.k + p.g.row(b, h, 0) + 16 * t;
+    const uint8_t* vb = p.v + p.g.row(b, h, 0) + (D / 8) * gr;
+    const float* ksp = p.ks + p.g.scale(b, h, 0);
+    const float* vsp = p.vs + p.g.scale(b, h, 0);
+    const int lb = 31 - __clz(p.g.blk);  // blk is a power of two
+    float* sc = p.scores ? p.scores + (((int64_t)b * per + pair) * p.g.capacity) * Gp : nullptr;
+
+    uint4 kw[NG][2][D / 64];
+    uint32_t vw[NG][4][VW];
+    float ksc[NG], vsc[NG];
+    auto load_k = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int tok = t0 + 16 * i + 8 * r + gr;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            kw[i][r][x] = tok < len ? ldg_stream16(kb + tok * p.g.st + 64 * x) : make_uint4(0, 0, 0, 0);
+        }
+        ksc[i] = t0 + 16 * i < len ? __ldg(ksp + ((t0 + 16 * i) >> lb)) : 1.0f;
+      }
+    };
+    auto load_v = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int tok = t0 + 16 * i + 2 * t + (r & 1) + 8 * (r >> 1);
+          if constexpr (D == 128) {
+            const uint4 w = tok < len ? ldg_stream16(vb + tok * p.g.st) : make_uint4(0, 0, 0, 0);
+            vw[i][r][0] = w.x;
+            vw[i][r][1] = w.y;
+            vw[i][r][2] = w.z;
+            vw[i][r][3] = w.w;
+          } else {
+            const uint2 w = tok < len ? ldg_stream8(vb + tok * p.g.st) : make_uint2(0, 0);
+            vw[i][r][0] = w.x;
+            vw[i][r][1] = w.y;
+          }
+        }
+        vsc[i] = t0 + 16 * i < len ? __ldg(vsp + ((t0 + 16 * i) >> lb)) : 0.0f;
+      }
+    };
+
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+    float unit = 0.0f, umax = 0.0f;  // O is in units of `unit`
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[a][s][e] = 0.0f;
+      m[a][0] = m[a][1] = -INFINITY;
+      l[a][0] = l[a][1] = 0.0f;
+    }
+    int t0 = j * UNIT + warp * STEP;
+    const int tend = min(len, (j + jn) * UNIT);
+    if (t0 < tend) {
+      load_k(t0);
+      load_v(t0);
+    }
+    for (; t0 < tend; t0 += UNIT) {
+      float sv[NG][NT][4];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[i][a][e] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint4 A = kw[i][0][s >> 2], B = kw[i][1][s >> 2];
+          const uint32_t wa = (s & 3) == 0 ? A.x : (s & 3) == 1 ? A.y : (s & 3) == 2 ? A.z : A.w;
+          const uint32_t wb = (s & 3) == 0 ? B.x : (s & 3) == 1 ? B.y : (s & 3) == 2 ? B.z : B.w;
+          const uint32_t a0 = e4m3x2_f16(wa), a2 = e4m3x2_f16(wa >> 16);
+          const uint32_t a1 = e4m3x2_f16(wb), a3 = e4m3x2_f16(wb >> 16);
+#pragma unroll
+          for (int a = 0; a < NT; ++a)
+            mma_16816(sv[i][a], a0, a1, a2, a3, qf[a][s].x, qf[a][s].y);
+        }
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sv[i][a][e] *= qs[a][e & 1] * ksc[i];
+            if (t0 + 16 * i + gr + 8 * (e >> 1) >= len) sv[i][a][e] = -INFINITY;
+          }
+      }
+      if (t0 + UNIT < tend) load_k(t0 + UNIT);
+      if (sc) {
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int tok = t0 + 16 * i + 8 * r + gr;
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+              if (tok < len && 8 * a + 2 * t < Gp)
+                *reinterpret_cast<float2*>(sc + (int64_t)tok * Gp + 8 * a + 2 * t) =
+                    make_float2(sv[i][a][2 * r], sv[i][a][2 * r + 1]);
+          }
+      }
+      // ---- running maximum and sum
+      float mx[NT][2];
+      bool grew = false;
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = sv[0][a][e];
+#pragma unroll
+          for (int i = 0; i < NG; ++i) x = fmaxf(x, fmaxf(sv[i][a][e], sv[i][a][e + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mx[a][e] = fmaxf(m[a][e], x);
+          grew |= mx[a][e] > m[a][e];
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int a = 0; a < NT; ++a) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float al = mx[a][e] > m[a][e] ? exp2f(m[a][e] - mx[a][e]) : 1.0f;
+            m[a][e] = mx[a][e];
+            l[a][e] *= al;
+            mx[a][e] = al;
+          }
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[a][s][e] *= mx[a][e & 1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        if (vsc[i] != unit && t0 + 16 * i < len) {
+          umax = fmaxf(umax, vsc[i]);
+          // a block 2^60 below the largest so far counts in that one's units
+          const float nu = vsc[i] < umax * 0x1p-60f ? umax * 0x1p-60f : vsc[i];
+          const float f = unit == 0.0f ? 0.0f : unit / nu;
+          unit = nu;
+#pragma unroll
+          for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[a][s][e] *= f;
+        }
+        const float ratio = vsc[i] == unit ? 1.0f : vsc[i] / unit;
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int a = 0; a < NT; ++a) {
+          float pr[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ref = m[a][e & 1] == -INFINITY ? 0.0f : m[a][e & 1];
+            pr[e] = ex2(sv[i][a][e] - ref);
+            l[a][e & 1] += pr[e];
+            pr[e] *= ratio;
+          }
+          b0[a] = transpose_8x8(pack_f16(pr[0], pr[1]));
+          b1[a] = transpose_8x8(pack_f16(pr[2], pr[3]));
+        }
+#pragma unroll
+        for (int x = 0; x < VW; ++x) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t lo = __byte_perm(vw[i][0][x], vw[i][1][x], y ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(vw[i][2][x], vw[i][3][x], y ? 0x7362 : 0x5140);
+            const uint32_t a0 = e4m3x2_f16(lo), a1 = e4m3x2_f16(lo >> 16);
+            const uint32_t a2 = e4m3x2_f16(hi), a3 = e4m3x2_f16(hi >> 16);
+#pragma unroll
+            for (int a = 0; a < NT; ++a) mma_16816(o[a][2 * x + y], a0, a1, a2, a3, b0[a], b1[a]);
+          }
+        }
+      }
+      if (t0 + UNIT < tend) load_v(t0 + UNIT);
+    }
+    // ---- the CTA's warps into one part
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[a][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (gr == 0) {
+          s_ml[warp][8 * a + 2 * t + e][0] = m[a][e];
+          s_ml[warp][8 * a + 2 * t + e][1] = x;
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            s_o[warp][8 * a + 2 * t + e][(D / 8) * gr + 2 * s + r] = o[a][s][2 * r + e] * unit;
+      }
+    __syncthreads();
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (seg > 0);
+    float* po = p.part_o + slot * p.Gc * D;
+    float* pm = p.part_ml + slot * p.Gc * 2;
+    for (int e = tid; e < heads * D; e += 32 * kKv8DecWarps) {
+      const int r = e / D, c = e % D;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kKv8DecWarps; ++w) M = fmaxf(M, s_ml[w][r][0]);
+      const float ref = M == -INFINITY ? 0.0f : M;
+      float acc = 0.0f, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKv8DecWarps; ++w) {
+        // a warp without tokens has the maximum -inf and adds 0
+        const float x = exp2f(s_ml[w][r][0] - ref);
+        acc += s_o[w][r][c] * x;
+        L += s_ml[w][r][1] * x;
+      }
+      po[e] = acc;
+      if (c == 0) {
+        pm[2 * r] = M;
+        pm[2 * r + 1] = L;
+      }
+    }
+    // next (kv head, part), or sequence
+    u += jn;
+    j = 0;
+    if (u < uend && ++pair == per) {
+      pair = 0;
+      do n = (int)ceil_div(p.g.len(p.len, ++b), UNIT);
+      while (n == 0);
+    }
+  }
+}
+
+// Parts of one (sequence, query head) merged, by 8 warps: out, lse, and what
+// the weights need.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8Dec p) {
+  constexpr int VEC = D / 32;
+  __shared__ float s_o[8][D], s_m[8], s_l[8];
+  __shared__ int tmp[16];
+  const int hq = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = hq / p.G, part = (hq % p.G) / p.Gc, r = (hq % p.G) % p.Gc;
+  const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
+  const int2 count = kv8_count<D>(p, b, tmp);
+  Kv8Plan plan;
+  plan.set(count.x, p.ctas);
+  const int u0 = count.y + (h * p.HG + part) * n;
+  const int a = n ? plan.owner(u0) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
+  pdl_wait();
+  float m = -INFINITY, l = 0.0f, o[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+#pragma unroll 4
+  for (int c = a + warp; c <= z; c += 8) {
+    const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);  // not its CTA's first part
+    const float* ml = p.part_ml + (slot * p.Gc + r) * 2;
+    const float mc = ml[0], lc = ml[1], mn = fmaxf(m, mc), ref = mn == -INFINITY ? 0.0f : mn;
+    const float x = exp2f(m - ref), y = exp2f(mc - ref);
+    const float* po = p.part_o + (slot * p.Gc + r) * D + VEC * lane;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = o[e] * x + po[e] * y;
+    l = l * x + lc * y;
+    m = mn;
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) s_o[warp][VEC * lane + e] = o[e];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  if (tid >= D) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
+  const float ref = M == -INFINITY ? 0.0f : M;
+  float acc = 0.0f, L = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float x = exp2f(s_m[w] - ref);
+    acc += s_o[w][tid] * x;
+    L += s_l[w] * x;
+  }
+  const int64_t bh = (int64_t)b * p.H + hq;
+  p.out[bh * D + tid] = f2h<DT>(n ? acc / L : 0.0f);
+  if (tid == 0) {
+    p.lse[bh] = n ? M * kLn2 + logf(L) : -INFINITY;
+    if (p.norm) {
+      p.norm[2 * bh] = M;
+      p.norm[2 * bh + 1] = 1.0f / L;
+    }
+  }
+}
+
+// weight[b, h, t] += the probabilities of token t, summed over the group's
+// heads, from the scores that the pass over the keys has left.
+constexpr int kKv8WeightTokens = 512;
+
+__global__ void __launch_bounds__(256) kv8_weight_kernel(const Kv8Dec p) {
+  const int h = blockIdx.y, b = blockIdx.z, len = p.g.len(p.len, b);
+  const int t0 = blockIdx.x * kKv8WeightTokens, Gp = (p.Gc + 1) & ~1;
+  if (t0 >= len) return;
+  pdl_wait();
+  for (int t = t0 + threadIdx.x; t < min(len, t0 + kKv8WeightTokens); t += 256) {
+    float sum = 0.0f;
+    for (int part = 0; part < p.HG; ++part) {
+      const int heads = min(p.Gc, p.G - part * p.Gc);
+      const float* s = p.scores +
+                       (((int64_t)(b * p.g.Hkv + h) * p.HG + part) * p.g.capacity + t) * Gp;
+      const float2* norm = reinterpret_cast<const float2*>(p.norm) + (int64_t)b * p.H + h * p.G +
+                           part * p.Gc;
+      for (int r = 0; r < heads; r += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(s + r);
+        const float2 n0 = norm[r];
+        sum += exp2f(x.x - n0.x) * n0.y;
+        if (r + 1 < heads) {
+          const float2 n1 = norm[r + 1];
+          sum += exp2f(x.y - n1.x) * n1.y;
+        }
+      }
+    }
+    p.weight[((int64_t)b * p.g.Hkv + h) * p.g.capacity + t] += sum;
+  }
 }
 
 // ------------------------------------------------------------------ evict --

@@ -345,6 +345,29 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ------------------------------------------------------ register MMA --
+
+// c += a b: a 16 x 16 and b 16 x 8 in fp16, c 16 x 8 in fp32, all in the
+// warp's registers.  Thread (g = lane / 4, t = lane % 4) holds a0 = (row g,
+// k 2t, 2t + 1), a1 = (row g + 8, same k), a2 and a3 = those rows at k + 8;
+// b0 = (k 2t, 2t + 1, column g), b1 = k + 8; c = (row g, columns 2t, 2t + 1),
+// (row g + 8, the same).
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 matrix of 16-bit values transposed: in, thread (g, t) holds row g,
+// columns 2t, 2t + 1; out, the same of the transpose.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
 // ------------------------------------------------------------ clusters --
 
 // Barrier of every thread of the cluster; shared memory written before it is

@@ -134,9 +134,9 @@ void launch_amax(const void* x, int64_t n_blocks, int G, uint32_t* out, cudaStre
 // while the previous kernel of the stream finishes; it waits for it
 // (pdl_wait) before touching anything that kernel may write.
 template <class Kernel, class... Args>
-cudaError_t launch_pdl(Kernel kernel, int grid, int threads, cudaStream_t st, Args... args) {
+cudaError_t launch_pdl(Kernel kernel, dim3 grid, int threads, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = st;
@@ -683,19 +683,48 @@ thrift_status kv8_append_impl(const void* kn, const void* vn, const Kv8Geom& g, 
   return launch_status();
 }
 
+// Parts and workspace of a decode step.  Returns the bytes.
+size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights, Kv8Dec* p,
+                       uint8_t* ws) {
+  const int G = H / Hkv, HG = (int)ceil_div(G, kKv8HeadGroup), Gc = (int)ceil_div(G, HG);
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    float* at = reinterpret_cast<float*>(ws + off);
+    off += (n * 4 + 255) & ~(size_t)255;
+    return at;
+  };
+  float* part_o = take((size_t)2 * kKv8MaxCtas * Gc * d);
+  float* part_ml = take((size_t)2 * kKv8MaxCtas * Gc * 2);
+  float* norm = weights ? take((size_t)B * H * 2) : nullptr;
+  float* scores =
+      weights ? take((size_t)B * Hkv * HG * capacity * ((Gc + 1) & ~1)) : nullptr;
+  if (p) {
+    p->H = H;
+    p->G = G;
+    p->HG = HG;
+    p->Gc = Gc;
+    p->part_o = part_o;
+    p->part_ml = part_ml;
+    p->norm = norm;
+    p->scores = scores;
+  }
+  return off;
+}
+
 template <int DT, int D>
-thrift_status kv8_decode_impl(const void* q, const Kv8Geom& g, int H, const void* k, const void* v,
-                              const float* ks, const float* vs, const int32_t* seq_len, float scale,
-                              float* weight, void* out, float* lse, cudaStream_t st) {
-  const uint16_t* qp = static_cast<const uint16_t*>(q);
-  const uint8_t* kp = static_cast<const uint8_t*>(k);
-  kv8_decode_kernel<DT, D><<<dim3(H, g.B), 128, 0, st>>>(
-      qp, g, H, kp, static_cast<const uint8_t*>(v), ks, vs, seq_len, scale,
-      static_cast<uint16_t*>(out), lse);
-  if (weight)
-    kv8_weight_kernel<DT, D><<<dim3((unsigned)ceil_div(g.capacity, 128), g.Hkv, g.B), 128, 0, st>>>(
-        qp, g, H, kp, ks, seq_len, scale, lse, weight);
-  return launch_status();
+thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
+  p.ctas = std::min(kKv8MaxCtas, kKv8DecCtas * sm_count());
+  const int threads = 32 * kKv8DecWarps;
+  if (p.Gc > 8)
+    kv8_decode_kernel<DT, D, 2><<<p.ctas, threads, 0, st>>>(p);
+  else
+    kv8_decode_kernel<DT, D, 1><<<p.ctas, threads, 0, st>>>(p);
+  cudaError_t e = launch_pdl(kv8_merge_kernel<DT, D>, dim3(p.H, p.g.B), 256, st, p);
+  if (e == cudaSuccess && p.weight)
+    e = launch_pdl(kv8_weight_kernel,
+                   dim3((unsigned)ceil_div(p.g.capacity, kKv8WeightTokens), p.g.Hkv, p.g.B), 256,
+                   st, p);
+  return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
 // --------------------------------------------------------------- linear --
@@ -1465,8 +1494,7 @@ thrift_status thrift_kv8_append(const void* k_new, const void* v_new, thrift_dty
 size_t thrift_kv8_decode_workspace_size(int B, int H, int Hkv, int capacity, int d,
                                         int accumulate) {
   if (kv8_shape(B, Hkv, d, 16, capacity) != THRIFT_OK || H <= 0 || H % Hkv) return 0;
-  (void)accumulate;
-  return 256;
+  return kv8_decode_plan(B, H, Hkv, capacity, d, accumulate != 0, nullptr, nullptr);
 }
 
 thrift_status thrift_kv8_decode(const void* q, thrift_dtype dt, int B, int H, int Hkv, int d,
@@ -1488,11 +1516,25 @@ thrift_status thrift_kv8_decode(const void* q, thrift_dtype dt, int B, int H, in
     return THRIFT_ERR_ARG;
   if (ws_bytes < thrift_kv8_decode_workspace_size(B, H, Hkv, capacity, d, weight != nullptr))
     return THRIFT_ERR_ARG;
-  const Kv8Geom g = kv8_geom(B, Hkv, blk, capacity, stride_b, stride_h, stride_t);
+  // units of work are counted in 32 bits
+  if ((int64_t)B * H * ceil_div(capacity, kv8_unit(d)) >= (int64_t)1 << 30)
+    return THRIFT_ERR_UNSUPPORTED;
+  Kv8Dec p = {};
+  kv8_decode_plan(B, H, Hkv, capacity, d, weight != nullptr, &p, static_cast<uint8_t*>(workspace));
+  p.g = kv8_geom(B, Hkv, blk, capacity, stride_b, stride_h, stride_t);
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.len = seq_len;
+  p.scale = scale * kLog2e;
+  p.weight = weight;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
   const auto run = dt == THRIFT_BF16 ? (d == 128 ? kv8_decode_impl<1, 128> : kv8_decode_impl<1, 64>)
                                      : (d == 128 ? kv8_decode_impl<0, 128> : kv8_decode_impl<0, 64>);
-  return run(q, g, H, k, v, k_scale, v_scale, seq_len, scale, weight, out, lse,
-             static_cast<cudaStream_t>(stream));
+  return run(p, static_cast<cudaStream_t>(stream));
 }
 
 size_t thrift_kv8_evict_workspace_size(int B, int Hkv, int capacity, int budget) {
