@@ -102,97 +102,103 @@ struct Kv8Geom {
   }
 };
 
-// Maximum over the CTA (every thread gets it); red holds one float per warp.
-__device__ __forceinline__ float block_max(float a, float* red) {
-  a = fmaxf(a, 0.0f);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  __syncthreads();  // red may still be read from the previous call
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = red[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) a = fmaxf(a, red[w]);
+// ----------------------------------------------------------------- append --
+//
+// A CTA of four warps takes a tile of max(64, blk) rows of one tensor (K or
+// V), kv head and sequence; each warp a quarter of it, whose values stay in
+// registers between the maximum and the encoding, so that they are read once.
+// A block's maximum is joined from its warps (one, two or four) in shared
+// memory: every row is loaded before the one barrier of the CTA.
+
+constexpr int kKv8Warps = 4, kKv8Threads = 32 * kKv8Warps;
+__host__ __device__ constexpr int kv8_tile(int blk) { return blk > 64 ? blk : 64; }
+
+// Maximum over the warps of this warp's block: `n` neighbours from a multiple
+// of n on.
+__device__ __forceinline__ float kv8_join(const float* red, int warp, int n) {
+  float a = red[warp & ~(n - 1)];
+  for (int i = 1; i < n; ++i) a = fmaxf(a, red[(warp & ~(n - 1)) + i]);
   return a;
 }
+__device__ __forceinline__ float warp_max(float a) {  // a >= 0
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+}
 
-// ----------------------------------------------------------------- append --
-
-constexpr int kKv8Threads = 256;
-
-// One CTA per (block that new tokens fall into, kv head, sequence): the
-// block's new rows stay in registers between the maximum and the encoding,
-// so the 16-bit values are read once; rows already there are re-encoded only
-// when the new maximum raises the scale.
-template <int DT, int D>
+// Rows already in a block are re-encoded only when the new ones raise its
+// scale.
+template <int DT, int D, int TILE>
 __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
     const uint16_t* __restrict__ kn, const uint16_t* __restrict__ vn, Kv8Geom g, int max_new,
     const int32_t* __restrict__ cache_len, const int32_t* __restrict__ n_new, uint8_t* k,
     uint8_t* v, float* ks, float* vs, float* __restrict__ weight) {
-  constexpr int TPR = D / 8;                  // threads a row (8 values each)
-  constexpr int RPP = kKv8Threads / TPR;      // rows a pass
-  constexpr int PASSES = 128 / RPP;           // blk <= 128
-  __shared__ float red[kKv8Threads / 32];
-  const int h = blockIdx.y, b = blockIdx.z;
+  constexpr int TPR = D / 8, RPP = 32 / TPR;  // threads a row (8 values each), rows a pass
+  constexpr int ROWS = TILE / kKv8Warps, PASSES = ROWS / RPP;
+  __shared__ float red[kKv8Warps];
+  const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 8 * (lane % TPR);
   const int len = g.len(cache_len, b);
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
-  const int j = len / g.blk + (int)blockIdx.x;
-  const int t0 = j * g.blk;
-  const int first = max(t0, len), last = min(end, t0 + g.blk);  // new rows [first, last)
-  if (first >= last) return;
-  const int row = threadIdx.x / TPR, c = 8 * (threadIdx.x % TPR);
-  if (weight)
-    for (int t = first + threadIdx.x; t < last; t += kKv8Threads)
-      weight[((int64_t)b * g.Hkv + h) * g.capacity + t] = 0.0f;
+  pdl_trigger();
+  const int64_t tile0 = (int64_t)(len / g.blk) * g.blk + (int64_t)blockIdx.x * TILE;
+  if (tile0 >= end || end == len) return;
+  const int w0 = (int)tile0 + warp * ROWS;  // this warp's rows [w0, w0 + ROWS)
+  const int wpb = g.blk > ROWS ? g.blk / ROWS : 1;
+  const uint16_t* src = (kv ? vn : kn) + ((int64_t)b * max_new * g.Hkv + h) * D + c;
+  uint8_t* codes = (kv ? v : k) + c;
+  if (weight && !kv)
+    for (int t = w0 + lane; t < w0 + ROWS; t += 32)
+      if (t >= len && t < end) weight[((int64_t)b * g.Hkv + h) * g.capacity + t] = 0.0f;
+  uint4 raw[PASSES];
+  float a = 0.0f;
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint16_t* src = (kv ? vn : kn) + ((int64_t)b * max_new * g.Hkv + h) * D + c;
-    uint8_t* codes = (kv ? v : k) + c;
-    float* scales = (kv ? vs : ks) + g.scale(b, h, j);
-    uint4 raw[PASSES];
-    float a = 0.0f;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int t = t0 + p * RPP + row;
-      raw[p] = make_uint4(0, 0, 0, 0);
-      if (t >= first && t < last)
-        raw[p] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
-    }
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      float x[8];
-      unpack8<DT>(raw[p], x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[i]) ? fabsf(x[i]) : 0.0f);
-    }
-    const float was = first > t0 ? *scales : 0.0f;
-    const float s = fmaxf(was, kv8_scale(block_max(a, red)));  // every thread has read was
-    const float inv = 1.0f / s;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int t = t0 + p * RPP + row;
-      if (t < first || t >= last) continue;
-      float x[8];
-      unpack8<DT>(raw[p], x);
-      *reinterpret_cast<uint2*>(codes + g.row(b, h, t)) = kv8_encode8(x, inv);
-    }
-    if (first > t0 && s != was) {
-      const float ratio = was / s;
-      for (int t = t0 + row; t < first; t += RPP) {
-        uint2* at = reinterpret_cast<uint2*>(codes + g.row(b, h, t));
-        float x[8];
-        kv8_decode8(*at, x);
-        *at = kv8_encode8(x, ratio);
-      }
-    }
-    if (threadIdx.x == 0) *scales = s;
+  for (int p = 0; p < PASSES; ++p) {
+    const int t = w0 + p * RPP + row;
+    raw[p] = make_uint4(0, 0, 0, 0);
+    if (t >= len && t < end)
+      raw[p] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
   }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    float x[8];
+    unpack8<DT>(raw[p], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[i]) ? fabsf(x[i]) : 0.0f);
+  }
+  const int t0 = w0 / g.blk * g.blk;  // the warp's block
+  float* scales = (kv ? vs : ks) + g.scale(b, h, 0) + w0 / g.blk;
+  const float was = t0 < len && w0 < end ? *scales : 0.0f;
+  if (lane == 0) red[warp] = 0.0f;
+  a = warp_max(a);
+  if (lane == 0) red[warp] = a;
+  __syncthreads();  // every warp has read its block's scale, too
+  if (t0 >= end) return;
+  const float s = fmaxf(was, kv8_scale(kv8_join(red, warp, wpb))), inv = 1.0f / s;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int t = w0 + p * RPP + row;
+    if (t < len || t >= end) continue;
+    float x[8];
+    unpack8<DT>(raw[p], x);
+    *reinterpret_cast<uint2*>(codes + g.row(b, h, t)) = kv8_encode8(x, inv);
+  }
+  if (t0 < len && s != was) {
+    const float ratio = was / s;
+    for (int t = w0 + row; t < min(len, w0 + ROWS); t += RPP) {
+      uint2* at = reinterpret_cast<uint2*>(codes + g.row(b, h, t));
+      float x[8];
+      kv8_decode8(*at, x);
+      *at = kv8_encode8(x, ratio);
+    }
+  }
+  if (lane == 0 && w0 == t0) *scales = s;
 }
 
 // new_len[b] = min(capacity, len + n).  new_len may be cache_len itself.
 __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_len,
                                    const int32_t* __restrict__ n_new, int32_t* new_len) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  pdl_wait();  // the append still reads cache_len
   if (b >= g.B) return;
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int len = min(g.capacity, max(0, cache_len[b]));
@@ -739,163 +745,260 @@ __device__ __forceinline__ uint32_t kv8_key(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kKv8SelThreads = 1024;
+constexpr int kKv8SelThreads = 1024, kKv8SelBins = 2048;
+constexpr int kKv8SelKeep = 16;  // tokens a thread holds in registers
 
 // kept[b, h, i], i < min(len, budget): the tokens that stay, ascending: the
 // first `sink`, the last `recent`, and the heaviest of the others, ties to
-// the lower token.  One CTA per (kv head, sequence): a radix select of 8 bits
-// a pass over the candidates' keys, then every warp writes the survivors of
-// one contiguous stretch.
+// the lower token.  A cluster of CTAs per (kv head, sequence), a warp a
+// contiguous stretch of tokens: a radix select of 11, 11 and 10 bits over the
+// candidates' keys, whose histograms are added over distributed shared memory
+// (every CTA arrives at the same digit), then every warp writes the survivors
+// of its stretch behind those of the lower ones.  REG: the keys stay in
+// registers from one read; else every pass reads them again.
+template <bool REG>
 __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
     const float* __restrict__ weight, Kv8Geom g, const int32_t* __restrict__ seq_len, int budget,
-    int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ len_out) {
-  __shared__ int hist[256], s_gt[32], s_eq[32];
+    int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ len_out, int cl) {
+  __shared__ uint32_t hist[2][kKv8SelBins];
+  __shared__ int s_gt[32], s_eq[32], s_warp[32];
+  __shared__ float s_count[2];  // of this CTA, as bits
   __shared__ uint32_t s_prefix;
   __shared__ int s_rem, s_done;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % cl, h = blockIdx.x / cl, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = g.len(seq_len, b);
   const int64_t bh = (int64_t)b * g.Hkv + h;
   const float* w = weight + bh * g.capacity;
   int32_t* out = kept + bh * budget;
-  if (h == 0 && tid == 0) len_out[b] = min(len, budget);
+  pdl_trigger();
+  if (blockIdx.x == 0 && tid == 0) len_out[b] = min(len, budget);
   if (len <= budget) {
-    for (int t = tid; t < len; t += kKv8SelThreads) out[t] = t;
+    for (int t = rank * kKv8SelThreads + tid; t < len; t += cl * kKv8SelThreads) out[t] = t;
     return;
   }
   const int lo = sink, hi = len - recent;  // candidates [lo, hi): more than are wanted
+  const int steps = (int)ceil_div(len, cl * kKv8SelThreads);  // of 32 tokens a warp
+  const int from = (int)min((int64_t)len, ((int64_t)rank * 32 + warp) * 32 * steps);
+  const int to = (int)min((int64_t)len, (int64_t)from + 32 * steps);
+  uint32_t key[REG ? kKv8SelKeep : 1];
+  if constexpr (REG) {
+#pragma unroll
+    for (int i = 0; i < kKv8SelKeep; ++i) {
+      const int t = from + 32 * i + lane;
+      key[i] = i < steps && t < to ? kv8_key(__ldg(w + t)) : 0u;
+    }
+  }
+  // f(token, key) for this thread's tokens, 32 consecutive ones a warp
+  auto each = [&](auto f) {
+    if constexpr (REG) {
+#pragma unroll
+      for (int i = 0; i < kKv8SelKeep; ++i)
+        if (i < steps) f(from + 32 * i + lane, key[i]);
+    } else {
+      for (int i = 0; i < steps; i += 8) {
+        uint32_t k8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int t = from + 32 * (i + j) + lane;
+          k8[j] = i + j < steps && t < to ? kv8_key(__ldg(w + t)) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < steps) f(from + 32 * (i + j) + lane, k8[j]);
+      }
+    }
+  };
   int rem = budget - sink - recent;
   uint32_t prefix = 0, pmask = 0;
   if (rem == 0) {
     prefix = pmask = 0xFFFFFFFFu;  // no key of a number is all ones: none is taken
   } else {
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      for (int i = tid; i < 256; i += kKv8SelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int base = lo; base < hi; base += kKv8SelThreads) {
-        const int t = base + tid;
-        const uint32_t key = t < hi ? kv8_key(__ldg(w + t)) : 0u;
-        const int digit = t < hi && (key & pmask) == prefix ? (int)((key >> shift) & 255u) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
-        if (digit >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+    for (int i = tid; i < 2 * kKv8SelBins; i += kKv8SelThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t mask = pass == 2 ? 1023u : 2047u;
+      uint32_t* mine = hist[pass & 1];
+      each([&](int t, uint32_t k) {
+        if (t >= lo && t < hi && t < to && (k & pmask) == prefix)
+          atomicAdd(&mine[(k >> shift) & mask], 1u);
+      });
+      if (cl > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      // bins from the top, two a thread
+      const int top = kKv8SelBins - 1 - 2 * tid;
+      uint32_t c0 = mine[top], c1 = mine[top - 1];
+      for (int r = 1; r < cl; ++r) {
+        const float* theirs = reinterpret_cast<const float*>(mine);
+        c0 += __float_as_uint(ld_cluster(theirs + top, (rank + r) % cl));
+        c1 += __float_as_uint(ld_cluster(theirs + top - 1, (rank + r) % cl));
       }
-      __syncthreads();
-      if (warp == 0) {
-        int64_t above;
-        const int sel = select_digit(hist, rem, &above);
-        if (lane == 0) {
-          s_rem = rem - (int)above;
-          s_prefix = prefix | ((uint32_t)sel << shift);
-          s_done = hist[sel] == rem - (int)above;
-        }
+      int upto = (int)(c0 + c1);
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
       }
+      if (lane == 31) s_warp[warp] = upto;
+      __syncthreads();
+      int before = 0;
+      for (int i = 0; i < warp; ++i) before += s_warp[i];
+      upto += before;
+      const int above0 = upto - (int)(c0 + c1), above1 = above0 + (int)c0;
+      if (above0 < rem && rem <= upto) {  // one thread
+        const bool first = rem <= above1;
+        const int n = (int)(first ? c0 : c1);
+        s_rem = rem - (first ? above0 : above1);
+        s_prefix = prefix | (uint32_t)(first ? top : top - 1) << shift;
+        s_done = n == s_rem;
+      }
+      // the other buffer, free since every CTA of the cluster has come here
+      if (pass == 1)
+        for (int i = tid; i < kKv8SelBins; i += kKv8SelThreads) hist[0][i] = 0;
       __syncthreads();
       prefix = s_prefix;
       rem = s_rem;
-      pmask |= 255u << shift;
+      pmask |= mask << shift;
       if (s_done) break;  // the whole bucket is taken: the lower bits decide nothing
-      __syncthreads();    // hist and s_done are rewritten by the next pass
     }
   }
   // A token stays if protected, above the threshold, or one of the first
   // `rem` at it.
-  const int per = (int)ceil_div(len, 32 * 32) * 32;
-  const int from = warp * per, to = min(len, from + per);
-  auto look = [&](int t, bool& gt, bool& eq) {
-    gt = eq = false;
-    if (t >= to) return;
-    if (t < lo || t >= hi) {
-      gt = true;
-      return;
-    }
-    const uint32_t key = kv8_key(__ldg(w + t)) & pmask;
-    gt = key > prefix;
-    eq = key == prefix;
+  auto look = [&](int t, uint32_t k, bool& gt, bool& eq) {
+    const bool in = t < to, free = t >= lo && t < hi;
+    gt = in && (!free || (k & pmask) > prefix);
+    eq = in && free && (k & pmask) == prefix;
   };
   int ngt = 0, neq = 0;
-  for (int t = from + lane; t - lane < to; t += 32) {
+  each([&](int t, uint32_t k) {
     bool gt, eq;
-    look(t, gt, eq);
+    look(t, k, gt, eq);
     ngt += __popc(__ballot_sync(0xffffffffu, gt));
     neq += __popc(__ballot_sync(0xffffffffu, eq));
-  }
+  });
   if (lane == 0) {
     s_gt[warp] = ngt;
     s_eq[warp] = neq;
   }
   __syncthreads();
   int gt0 = 0, eq0 = 0;
+  if (cl > 1) {
+    int all_gt = 0, all_eq = 0;
+    for (int i = 0; i < 32; ++i) {
+      all_gt += s_gt[i];
+      all_eq += s_eq[i];
+    }
+    if (tid == 0) {
+      s_count[0] = __int_as_float(all_gt);
+      s_count[1] = __int_as_float(all_eq);
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      gt0 += __float_as_int(ld_cluster(s_count, r));
+      eq0 += __float_as_int(ld_cluster(s_count + 1, r));
+    }
+  }
   for (int i = 0; i < warp; ++i) {
     gt0 += s_gt[i];
     eq0 += s_eq[i];
   }
   const unsigned below = (1u << lane) - 1u;
-  for (int t = from + lane; t - lane < to; t += 32) {
+  each([&](int t, uint32_t k) {
     bool gt, eq;
-    look(t, gt, eq);
+    look(t, k, gt, eq);
     const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
     const int e = eq0 + __popc(me & below);
     // survivors before this token: all above, and the first rem of the equal
     if (gt || (eq && e < rem)) out[gt0 + __popc(mg & below) + min(e, rem)] = t;
     gt0 += __popc(mg);
     eq0 += __popc(me);
-  }
+  });
+  if (cl > 1) cluster_sync();  // nobody leaves while its counts are read
 }
 
-// One CTA per (block of the new cache, kv head, sequence): the kept tokens'
-// values, re-encoded under the new block's own scale.
-template <int D>
+// The kept tokens of a tile of the new cache, re-encoded under the scales of
+// their new blocks: warps and tiles as in the append.  The maximum is taken
+// over fp16 pairs (codes are exact fp16 numbers, and the larger of a number
+// and a NaN is the number), one product with its scale a row.
+template <int D, int TILE>
 __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
     Kv8Geom g, Kv8Geom go, const uint8_t* __restrict__ k, const uint8_t* __restrict__ v,
     const float* __restrict__ ks, const float* __restrict__ vs, const float* __restrict__ weight,
     const int32_t* __restrict__ seq_len, const int32_t* __restrict__ kept, int budget,
     uint8_t* __restrict__ ko, uint8_t* __restrict__ vo, float* __restrict__ kso,
     float* __restrict__ vso, float* __restrict__ wo) {
-  constexpr int TPR = D / 8, RPP = kKv8Threads / TPR, PASSES = 128 / RPP;
-  __shared__ float red[kKv8Threads / 32];
-  const int j = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  constexpr int TPR = D / 16, RPP = 32 / TPR;  // threads a row (16 codes each), rows a pass
+  constexpr int ROWS = TILE / kKv8Warps, PASSES = ROWS / RPP;
+  __shared__ float red[kKv8Warps];
+  const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 16 * (lane % TPR);
   const int n = min(g.len(seq_len, b), budget);
-  const int i0 = j * g.blk;
-  if (i0 >= n) return;
-  const int i1 = min(n, i0 + g.blk);
-  const int row = threadIdx.x / TPR, c = 8 * (threadIdx.x % TPR);
+  const int w0 = (int)blockIdx.x * TILE + warp * ROWS;
+  if ((int)blockIdx.x * TILE >= n) return;
+  const int wpb = g.blk > ROWS ? g.blk / ROWS : 1;
   const int64_t bh = (int64_t)b * g.Hkv + h;
+  const uint8_t* codes = (kv ? v : k) + c;
+  const float* scales = (kv ? vs : ks) + g.scale(b, h, 0);
+  const int lb = 31 - __clz(g.blk);  // blk is a power of two
+  pdl_wait();
   int src[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int i = i0 + p * RPP + row;
-    src[p] = i < i1 ? __ldg(kept + bh * budget + i) : -1;
-    if (src[p] >= 0 && c == 0) wo[bh * go.capacity + i] = __ldg(weight + bh * g.capacity + src[p]);
+    const int i = w0 + p * RPP + row;
+    src[p] = i < n ? __ldcg(kept + bh * budget + i) : -1;
   }
+  uint4 w[PASSES];
+  float s[PASSES];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint8_t* codes = (kv ? v : k) + c;
-    const float* scales = kv ? vs : ks;
-    float x[PASSES][8];
-    float a = 0.0f;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      uint2 w = make_uint2(0, 0);
-      float s = 0.0f;
-      if (src[p] >= 0) {
-        w = __ldg(reinterpret_cast<const uint2*>(codes + g.row(b, h, src[p])));
-        s = __ldg(scales + g.scale(b, h, src[p] / g.blk));
-      }
-      kv8_decode8(w, x[p]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[p][e] *= s;
-        a = fmaxf(a, finite_f(x[p][e]) ? fabsf(x[p][e]) : 0.0f);
-      }
+  for (int p = 0; p < PASSES; ++p) {
+    w[p] = make_uint4(0, 0, 0, 0);
+    s[p] = 0.0f;
+    if (src[p] >= 0) {
+      w[p] = ldg_stream16(codes + g.row(b, h, src[p]));
+      s[p] = __ldg(scales + (src[p] >> lb));
+      if (!kv && c == 0)
+        wo[bh * go.capacity + w0 + p * RPP + row] = __ldg(weight + bh * g.capacity + src[p]);
     }
-    const float s = kv8_scale(block_max(a, red)), inv = kv8_inv(s);
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p)
-      if (src[p] >= 0)
-        *reinterpret_cast<uint2*>((kv ? vo : ko) + c + go.row(b, h, i0 + p * RPP + row)) =
-            kv8_encode8(x[p], inv);
-    if (threadIdx.x == 0) (kv ? vso : kso)[go.scale(b, h, j)] = s;
   }
+  float a = 0.0f;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const uint32_t x[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+    __half2 top = __float2half2_rn(0.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = e4m3x2_f16(x[j]), hi = e4m3x2_f16(x[j] >> 16);
+      top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&lo)));
+      top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&hi)));
+    }
+    const float2 f = __half22float2(top);
+    const float y = fmaxf(f.x, f.y) * fabsf(s[p]);
+    a = fmaxf(a, finite_f(y) ? y : 0.0f);
+  }
+  a = warp_max(a);
+  if (lane == 0) red[warp] = a;
+  __syncthreads();
+  if (w0 / g.blk * g.blk >= n) return;
+  const float so = kv8_scale(kv8_join(red, warp, wpb)), inv = kv8_inv(so);
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    if (src[p] < 0) continue;
+    float x[8], y[8];
+    kv8_decode8(make_uint2(w[p].x, w[p].y), x);
+    kv8_decode8(make_uint2(w[p].z, w[p].w), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] *= s[p];
+      y[e] *= s[p];
+    }
+    const uint2 lo = kv8_encode8(x, inv), hi = kv8_encode8(y, inv);
+    *reinterpret_cast<uint4*>((kv ? vo : ko) + c + go.row(b, h, w0 + p * RPP + row)) =
+        make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+  if (lane == 0 && w0 % g.blk == 0) (kv ? vso : kso)[go.scale(b, h, w0 >> lb)] = so;
 }
 
 }  // namespace thrift

@@ -635,7 +635,7 @@ thrift_status kv8_shape(int B, int Hkv, int d, int blk, int capacity) {
   if (B <= 0 || Hkv <= 0 || d <= 0 || blk <= 0 || capacity <= 0) return THRIFT_ERR_ARG;
   if ((d != 64 && d != 128) || (blk != 16 && blk != 32 && blk != 64 && blk != 128))
     return THRIFT_ERR_UNSUPPORTED;
-  if (B > 65535 || Hkv > 65535 || capacity > (1 << 30)) return THRIFT_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 32767 || capacity > (1 << 30)) return THRIFT_ERR_UNSUPPORTED;
   return THRIFT_OK;
 }
 
@@ -673,14 +673,41 @@ thrift_status kv8_append_impl(const void* kn, const void* vn, const Kv8Geom& g, 
                               const int32_t* cache_len, const int32_t* n_new, void* k, void* v,
                               float* ks, float* vs, float* weight, int32_t* new_len,
                               cudaStream_t st) {
-  const int nb = (int)ceil_div((int64_t)max_new - 1, g.blk) + 1;  // blocks max_new tokens can touch
-  kv8_append_kernel<DT, D><<<dim3(nb, g.Hkv, g.B), kKv8Threads, 0, st>>>(
+  const int tile = kv8_tile(g.blk);
+  // from the start of the block that the first token joins
+  const int tiles = (int)ceil_div((int64_t)max_new + g.blk - 1, tile);
+  const auto kernel = tile > 64 ? kv8_append_kernel<DT, D, 128> : kv8_append_kernel<DT, D, 64>;
+  kernel<<<dim3(tiles, 2 * g.Hkv, g.B), kKv8Threads, 0, st>>>(
       static_cast<const uint16_t*>(kn), static_cast<const uint16_t*>(vn), g, max_new, cache_len,
       n_new, static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), ks, vs, weight);
-  if (new_len)
-    kv8_advance_kernel<<<(int)ceil_div(g.B, kThreads), kThreads, 0, st>>>(g, max_new, cache_len,
-                                                                         n_new, new_len);
+  if (new_len &&
+      launch_pdl(kv8_advance_kernel, dim3((unsigned)ceil_div(g.B, kThreads)), kThreads, st, g,
+                 max_new, cache_len, n_new, new_len) != cudaSuccess)
+    return THRIFT_ERR_CUDA;
   return launch_status();
+}
+
+// The survivors of every (sequence, kv head): CTAs of a cluster until a
+// thread holds all its keys (131072 tokens), or reads them again a pass.
+cudaError_t kv8_select_launch(const float* weight, const Kv8Geom& g, const int32_t* seq_len,
+                              int budget, int sink, int recent, int32_t* kept, int32_t* len_out,
+                              cudaStream_t st) {
+  int cl = 1;
+  while (cl < 8 && cl * 4 * kKv8SelThreads < g.capacity) cl *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(g.Hkv * cl, g.B);
+  cfg.blockDim = dim3(kKv8SelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)cl, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = cl > 1;
+  const auto kernel = (int64_t)cl * kKv8SelThreads * kKv8SelKeep >= g.capacity
+                          ? kv8_select_kernel<true>
+                          : kv8_select_kernel<false>;
+  return cudaLaunchKernelEx(&cfg, kernel, weight, g, seq_len, budget, sink, recent, kept, len_out,
+                            cl);
 }
 
 // Parts and workspace of a decode step.  Returns the bytes.
@@ -1586,15 +1613,17 @@ thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int
       kv8_geom(B, Hkv, blk, out_capacity, out_stride_b, out_stride_h, out_stride_t);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* kept = static_cast<int32_t*>(workspace);
-  kv8_select_kernel<<<dim3(Hkv, B), kKv8SelThreads, 0, st>>>(weight, g, seq_len, budget, sink,
-                                                             recent, kept, len_out);
-  const dim3 grid((unsigned)ceil_div(budget, blk), Hkv, B);
-  const auto gather = d == 128 ? kv8_gather_kernel<128> : kv8_gather_kernel<64>;
-  gather<<<grid, kKv8Threads, 0, st>>>(
-      g, go, static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_scale, v_scale,
-      weight, seq_len, kept, budget, static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out),
-      k_scale_out, v_scale_out, weight_out);
-  return launch_status();
+  cudaError_t e = kv8_select_launch(weight, g, seq_len, budget, sink, recent, kept, len_out, st);
+  if (e != cudaSuccess) return THRIFT_ERR_CUDA;
+  const bool big = kv8_tile(blk) > 64;
+  const auto gather = d == 128 ? (big ? kv8_gather_kernel<128, 128> : kv8_gather_kernel<128, 64>)
+                               : (big ? kv8_gather_kernel<64, 128> : kv8_gather_kernel<64, 64>);
+  e = launch_pdl(gather, dim3((unsigned)ceil_div(budget, kv8_tile(blk)), 2 * Hkv, B), kKv8Threads,
+                 st, g, go, static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v),
+                 k_scale, v_scale, weight, seq_len, (const int32_t*)kept, budget,
+                 static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out), k_scale_out,
+                 v_scale_out, weight_out);
+  return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
 // -------------------------------------------------------------- linear --
