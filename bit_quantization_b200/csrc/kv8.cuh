@@ -194,6 +194,66 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
   if (lane == 0 && w0 == t0) *scales = s;
 }
 
+// The few tokens of a generation step: one CTA a sequence, a warp a tensor
+// and kv head, which takes a block at a time.  It ends with the new length
+// (every warp has read the old one by then), so that a step is one launch.
+constexpr int kKv8StepTokens = 8;
+
+template <int DT, int D>
+__global__ void __launch_bounds__(1024) kv8_append_step_kernel(
+    const uint16_t* __restrict__ kn, const uint16_t* __restrict__ vn, Kv8Geom g, int max_new,
+    const int32_t* cache_len, const int32_t* __restrict__ n_new, uint8_t* k, uint8_t* v, float* ks,
+    float* vs, float* __restrict__ weight, int32_t* new_len) {
+  constexpr int TPR = D / 8, RPP = 32 / TPR, PASSES = kKv8StepTokens / RPP;
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane / TPR, c = 8 * (lane % TPR);
+  const int len = min(g.capacity, max(0, cache_len[b]));
+  const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
+  const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
+  for (int u = warp; u < 2 * g.Hkv; u += blockDim.x >> 5) {
+    const int h = u >> 1, kv = u & 1;
+    const uint16_t* src = (kv ? vn : kn) + ((int64_t)b * max_new * g.Hkv + h) * D + c;
+    uint8_t* codes = (kv ? v : k) + g.row(b, h, 0);
+    float* scales = (kv ? vs : ks) + g.scale(b, h, 0);
+    if (weight && !kv && len + lane < end)
+      weight[((int64_t)b * g.Hkv + h) * g.capacity + len + lane] = 0.0f;
+    for (int t0 = len / g.blk * g.blk; t0 < end; t0 += g.blk) {
+      const int first = max(t0, len), last = min(end, t0 + g.blk);
+      if (first >= last) break;
+      float x[PASSES][8], a = 0.0f;
+      const float was = t0 < len ? scales[t0 / g.blk] : 0.0f;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int t = first + p * RPP + row;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (t < last) raw = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
+        unpack8<DT>(raw, x[p]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[p][i]) ? fabsf(x[p][i]) : 0.0f);
+      }
+      const float s = fmaxf(was, kv8_scale(warp_max(a))), inv = 1.0f / s;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int t = first + p * RPP + row;
+        if (t < last) *reinterpret_cast<uint2*>(codes + t * g.st + c) = kv8_encode8(x[p], inv);
+      }
+      if (t0 < len && s != was) {
+        const float ratio = was / s;
+#pragma unroll 8
+        for (int t = t0 + row; t < len; t += RPP) {
+          uint2* at = reinterpret_cast<uint2*>(codes + t * g.st + c);
+          float y[8];
+          kv8_decode8(*at, y);
+          *at = kv8_encode8(y, ratio);
+        }
+      }
+      if (lane == 0) scales[t0 / g.blk] = s;
+    }
+  }
+  __syncthreads();
+  if (new_len && threadIdx.x == 0) new_len[b] = end;
+}
+
 // new_len[b] = min(capacity, len + n).  new_len may be cache_len itself.
 __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_len,
                                    const int32_t* __restrict__ n_new, int32_t* new_len) {

@@ -673,6 +673,13 @@ thrift_status kv8_append_impl(const void* kn, const void* vn, const Kv8Geom& g, 
                               const int32_t* cache_len, const int32_t* n_new, void* k, void* v,
                               float* ks, float* vs, float* weight, int32_t* new_len,
                               cudaStream_t st) {
+  if (max_new <= kKv8StepTokens) {
+    // measured at 64 sequences x 8 heads and one token: 3.2 us against 6.1
+    kv8_append_step_kernel<DT, D><<<g.B, 32 * std::min(32, 2 * g.Hkv), 0, st>>>(
+        static_cast<const uint16_t*>(kn), static_cast<const uint16_t*>(vn), g, max_new, cache_len,
+        n_new, static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), ks, vs, weight, new_len);
+    return launch_status();
+  }
   const int tile = kv8_tile(g.blk);
   // from the start of the block that the first token joins
   const int tiles = (int)ceil_div((int64_t)max_new + g.blk - 1, tile);

@@ -6,7 +6,9 @@ fallback: a missing library, a missing CUDA device or a failing call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import functools
 import os
 from typing import Optional
 
@@ -192,12 +194,17 @@ def _need_cuda(*ts):
             raise ThriftError("tensors must be contiguous")
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream's handle on device ``index``."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _stream(t: torch.Tensor):
-    return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return C.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def device_status(reset: bool = False) -> int:
@@ -213,11 +220,14 @@ def stream_status(stream: Optional[torch.cuda.Stream] = None, reset: bool = Fals
         return lib().thrift_stream_status(C.c_void_p(st.cuda_stream), int(reset))
 
 
+_stay = contextlib.nullcontext()
+
+
 def _on(t: torch.Tensor):
     """Makes the tensor's device current around a library call (the library
     resolves per-device state, such as the no-allocation scratch address, on
     the current device)."""
-    return torch.cuda.device(t.device)
+    return _stay if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def kernel_timer_enable(enable: bool):
@@ -253,13 +263,16 @@ class Workspace:
         self.bufs = {}
 
     def get(self, nbytes: int, device) -> torch.Tensor:
-        nbytes = max(int(nbytes), 256)
         device = torch.device(device)
-        stream = torch.cuda.current_stream(device)
-        key = (device.index, stream.cuda_stream)
+        return self.of(nbytes, device.index)
+
+    def of(self, nbytes: int, index: int) -> torch.Tensor:
+        key = (index, _raw_stream(index))
         buf = self.bufs.get(key)
         if buf is None or buf.numel() < nbytes:
+            nbytes, device = max(int(nbytes), 256), torch.device("cuda", index)
             self.bufs.pop(key, None)
+            stream = torch.cuda.current_stream(device)
             with torch.cuda.device(device), torch.cuda.stream(stream):
                 buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
             self.bufs[key] = buf
@@ -613,46 +626,73 @@ _F8 = torch.float8_e4m3fn
 
 
 def _same_device(first, *ts):
-    """Every given tensor on the CUDA device of the first."""
-    if not first.is_cuda:
+    """Every given tensor on the CUDA device of the first, whose index is
+    returned."""
+    index = first.get_device()
+    if index < 0:
         raise ThriftError("tensors must live on a CUDA device")
     for t in ts:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ThriftError(f"tensors must live on one device: {t.device} and {first.device}")
+    return index
 
 
 def _vector(t, n, dtype, name):
     """A contiguous auxiliary tensor of n elements."""
-    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+    if t is not None and (t.dtype is not dtype or t.numel() != n or not t.is_contiguous()):
         raise ThriftError(f"{name} must be contiguous {dtype} with {n} elements, got {t.dtype} "
                           f"{tuple(t.shape)}")
 
 
-def _scratch(nbytes, device):
-    """Workspace of a call: the stream's own buffer, or, under graph capture,
-    memory of the graph's pool (two graphs never share it, and it lives as
-    long as the graph)."""
+def _dense(t, shape, dtype, name):
+    """A contiguous tensor of a given shape and type, or None."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        raise ThriftError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, got "
+                          f"{t.dtype} {tuple(t.shape)}")
+
+
+def _scratch(nbytes, index):
+    """Workspace of a call on device ``index``: the stream's own buffer, or,
+    under graph capture, memory of the graph's pool (two graphs never share
+    it, and it lives as long as the graph)."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-    return _ws.get(nbytes, device)
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
+    return _ws.of(nbytes, index)
+
+
+def _own_bytes(workspace):
+    """Checks a workspace of the caller's."""
+    if workspace is not None and (workspace.dtype is not torch.uint8 or
+                                  not workspace.is_contiguous()):
+        raise ThriftError("workspace must be contiguous uint8")
+
+
+def _call(index, what, fn, *args):
+    """A library call with device ``index`` current (see _on)."""
+    if index == torch.cuda.current_device():
+        code = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args)
+    if code != OK:
+        _check(code, what)
 
 
 def _kv8_cache(k, v, k_scale, v_scale, blk, what=""):
     """Checks the four tensors of an 8-bit cache; returns B, Hkv, capacity, d
     and the codes' strides (batch, head, token) in bytes."""
-    if k.dim() != 4 or k.dtype != _F8 or v.dtype != _F8 or v.shape != k.shape:
+    if k.dim() != 4 or k.dtype is not _F8 or v.dtype is not _F8 or v.shape != k.shape:
         raise ThriftError(f"k{what}, v{what} must be {_F8} [B, Hkv, capacity, d] of one shape")
-    if k.stride() != v.stride() or k.stride(3) != 1:
+    strides = k.stride()
+    if v.stride() != strides or strides[3] != 1:
         raise ThriftError(f"k{what}, v{what} must have one layout, the last axis contiguous")
     B, Hkv, cap, d = k.shape
-    if blk not in (16, 32, 64, 128) or d not in (64, 128):
+    if min(B, Hkv, cap) < 1 or blk not in (16, 32, 64, 128) or d not in (64, 128):
         raise ThriftError("the 8-bit cache supports blk 16, 32, 64, 128 and d 64, 128")
     shape = (B, Hkv, -(-cap // blk))
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _check_like(t, shape, torch.float32, name + what)
-        if not t.is_contiguous():
-            raise ThriftError(f"{name}{what} must be contiguous")
-    return B, Hkv, cap, d, k.stride()[:3]
+    _dense(k_scale, shape, torch.float32, "k_scale" + what)
+    _dense(v_scale, shape, torch.float32, "v_scale" + what)
+    return B, Hkv, cap, d, strides[:3]
 
 
 def thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new=None, blk=64,
@@ -673,15 +713,16 @@ def thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new=Non
     _vector(n_new, B, torch.int32, "n_new")
     _vector(new_len, B, torch.int32, "new_len")
     _vector(weight, B * Hkv * cap, torch.float32, "weight")
-    _same_device(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new, weight, new_len)
-    _need_cuda(k_new, v_new)
-    with _on(k_new):
-        _check(lib().thrift_kv8_append(_ptr(k_new), _ptr(v_new), _dt(k_new), B, Hkv, d, blk, cap,
-                                       *st, _ptr(cache_len), _ptr(n_new), k_new.shape[1], _ptr(k),
-                                       _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight),
-                                       _ptr(new_len), _stream(k_new)), "thrift_kv8_append")
+    _dense(k_new, k_new.shape, k_new.dtype, "k_new")
+    _dense(v_new, v_new.shape, v_new.dtype, "v_new")
+    index = _same_device(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new, weight, new_len)
+    _call(index, "thrift_kv8_append", lib().thrift_kv8_append, k_new.data_ptr(), v_new.data_ptr(),
+          _dt(k_new), B, Hkv, d, blk, cap, *st, cache_len.data_ptr(), _ptr(n_new),
+          k_new.shape[1], k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+          _ptr(weight), _ptr(new_len), _raw_stream(index))
 
 
+@functools.lru_cache(maxsize=1024)
 def kv8_decode_workspace_size(B, H, Hkv, capacity, d=128, accumulate=False) -> int:
     return int(lib().thrift_kv8_decode_workspace_size(B, H, Hkv, capacity, d, int(accumulate)))
 
@@ -697,28 +738,29 @@ def thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk=64, scale=None, we
     if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % Hkv:
         raise ThriftError(f"q must be [{B}, H (a multiple of {Hkv}), {d}]")
     H = q.shape[1]
-    _check_like(out, q.shape, q.dtype, "out")
-    _check_like(lse, (B, H), torch.float32, "lse")
+    _dense(q, q.shape, q.dtype, "q")
+    _dense(out, q.shape, q.dtype, "out")
+    _dense(lse, (B, H), torch.float32, "lse")
     _vector(seq_len, B, torch.int32, "seq_len")
     _vector(weight, B * Hkv * cap, torch.float32, "weight")
-    _same_device(q, k, v, k_scale, v_scale, seq_len, weight, out, lse, workspace)
-    _need_cuda(q, *(t for t in (out, lse, workspace) if t is not None))
+    _own_bytes(workspace)
+    index = _same_device(q, k, v, k_scale, v_scale, seq_len, weight, out, lse, workspace)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    with _on(q):
-        if workspace is None:
-            need = kv8_decode_workspace_size(B, H, Hkv, cap, d, weight is not None)
-            workspace = _scratch(need, q.device)
-        _check(lib().thrift_kv8_decode(_ptr(q), _dt(q), B, H, Hkv, d, blk, cap, *st, _ptr(k),
-                                       _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(seq_len),
-                                       d ** -0.5 if scale is None else float(scale), _ptr(weight),
-                                       _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                       _stream(q)), "thrift_kv8_decode")
+        lse = q.new_empty((B, H), dtype=torch.float32)
+    if workspace is None:
+        workspace = _scratch(kv8_decode_workspace_size(B, H, Hkv, cap, d, weight is not None),
+                             index)
+    _call(index, "thrift_kv8_decode", lib().thrift_kv8_decode, q.data_ptr(), _dt(q), B, H, Hkv, d,
+          blk, cap, *st, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+          seq_len.data_ptr(), d ** -0.5 if scale is None else float(scale), _ptr(weight),
+          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+          _raw_stream(index))
     return out, lse
 
 
+@functools.lru_cache(maxsize=1024)
 def kv8_evict_workspace_size(B, Hkv, capacity, budget) -> int:
     return int(lib().thrift_kv8_evict_workspace_size(B, Hkv, capacity, budget))
 
@@ -742,17 +784,17 @@ def thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_o
     _vector(weight_out, B * Hkv * cap_o, torch.float32, "weight_out")
     _vector(seq_len, B, torch.int32, "seq_len")
     _vector(len_out, B, torch.int32, "len_out")
-    _same_device(k, v, k_scale, v_scale, weight, seq_len, k_out, v_out, k_scale_out, v_scale_out,
-                 weight_out, len_out, workspace)
-    with _on(k):
-        if workspace is None:
-            workspace = _scratch(kv8_evict_workspace_size(B, Hkv, cap, budget), k.device)
-        _check(lib().thrift_kv8_evict(B, Hkv, d, blk, cap, *st, _ptr(k), _ptr(v), _ptr(k_scale),
-                                      _ptr(v_scale), _ptr(weight), _ptr(seq_len), budget, sink,
-                                      recent, cap_o, *sto, _ptr(k_out), _ptr(v_out),
-                                      _ptr(k_scale_out), _ptr(v_scale_out), _ptr(weight_out),
-                                      _ptr(len_out), _ptr(workspace), workspace.numel(),
-                                      _stream(k)), "thrift_kv8_evict")
+    _own_bytes(workspace)
+    index = _same_device(k, v, k_scale, v_scale, weight, seq_len, k_out, v_out, k_scale_out,
+                         v_scale_out, weight_out, len_out, workspace)
+    if workspace is None:
+        workspace = _scratch(kv8_evict_workspace_size(B, Hkv, cap, budget), index)
+    _call(index, "thrift_kv8_evict", lib().thrift_kv8_evict, B, Hkv, d, blk, cap, *st,
+          k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), weight.data_ptr(),
+          seq_len.data_ptr(), budget, sink, recent, cap_o, *sto, k_out.data_ptr(),
+          v_out.data_ptr(), k_scale_out.data_ptr(), v_scale_out.data_ptr(),
+          weight_out.data_ptr(), len_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+          _raw_stream(index))
 
 
 class KV8Cache:
@@ -810,6 +852,7 @@ class KV8Cache:
 
 # ----------------------------------------------------------------- linear --
 
+@functools.lru_cache(maxsize=1024)
 def nvfp4_linear_workspace_size(M, N, K) -> int:
     return int(lib().nvfp4_linear_workspace_size(M, N, K))
 
@@ -823,26 +866,26 @@ def nvfp4_linear(x, codes, scales, tensor_scale, out=None, workspace=None):
     M, K = x.shape
     N = codes.shape[0]
     dt = _dt(x)
-    _check_like(codes, (N, K // 2), torch.uint8, "codes")
-    _check_like(scales, (N, K // 16), torch.uint8, "scales")
-    _check_like(out, (M, N), x.dtype, "out")
-    if tensor_scale.dtype != torch.float32 or tensor_scale.numel() < 1:
+    _dense(x, (M, K), x.dtype, "x")
+    _dense(codes, (N, K // 2), torch.uint8, "codes")
+    _dense(scales, (N, K // 16), torch.uint8, "scales")
+    _dense(out, (M, N), x.dtype, "out")
+    _own_bytes(workspace)
+    if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() < 1:
         raise ThriftError("tensor_scale must be float32 with at least one element")
     if M > 64 or K == 0 or K % 32 or K > 1 << 19:
         raise ThriftError("nvfp4_linear supports at most 64 rows and K a multiple of 32 up to "
                           "524288")
-    _same_device(x, codes, scales, tensor_scale, out, workspace)
-    _need_cuda(x, codes, scales, *(t for t in (out, workspace) if t is not None))
+    index = _same_device(x, codes, scales, tensor_scale, out, workspace)
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, N))
     if M == 0 or N == 0:
         return out
-    with _on(x):
-        if workspace is None:
-            workspace = _scratch(nvfp4_linear_workspace_size(M, N, K), x.device)
-        _check(lib().nvfp4_linear(_ptr(x), dt, M, N, K, _ptr(codes), _ptr(scales),
-                                  _ptr(tensor_scale), _ptr(out), _ptr(workspace),
-                                  workspace.numel(), _stream(x)), "nvfp4_linear")
+    if workspace is None:
+        workspace = _scratch(nvfp4_linear_workspace_size(M, N, K), index)
+    _call(index, "nvfp4_linear", lib().nvfp4_linear, x.data_ptr(), dt, M, N, K, codes.data_ptr(),
+          scales.data_ptr(), tensor_scale.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+          workspace.numel(), _raw_stream(index))
     return out
 
 
