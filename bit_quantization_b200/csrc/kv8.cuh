@@ -24,11 +24,6 @@ __device__ __forceinline__ float kv8_scale(float a) {
   return __uint_as_float((uint32_t)(max(e, -120) + 127) << 23);
 }
 
-// 1 / s for a power of two s in [2^-120, 2^120] (exact).
-__device__ __forceinline__ float kv8_inv(float s) {
-  return __uint_as_float((254u << 23) - __float_as_uint(s));
-}
-
 // Two fp32 values -> two E4M3 codes (lo in the low byte), round to nearest
 // even, saturating; NaN -> 0x7F.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -73,6 +68,22 @@ __device__ __forceinline__ void kv8_decode8(uint2 c, float (&x)[8]) {
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;
   }
+}
+
+// Eight finite 16-bit values -> eight codes under 1 / scale.
+template <int DT>
+__device__ __forceinline__ uint2 kv8_encode8_finite(uint4 r, float inv) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = e4m3x2(h2f<DT>((uint16_t)(w[i] & 0xFFFFu)) * inv, h2f<DT>((uint16_t)(w[i] >> 16)) * inv);
+  return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+}
+
+// Larger of |x| in each 16-bit half, as bits (infinities and NaN on top).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t w) {
+  return __vmaxu2(a, w & 0x7FFF7FFFu);
 }
 
 template <int DT>
@@ -158,12 +169,22 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
     if (t >= len && t < end)
       raw[p] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
   }
+  uint32_t bits = 0;
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    float x[8];
-    unpack8<DT>(raw[p], x);
+  for (int p = 0; p < PASSES; ++p)
+    bits = max_abs2(max_abs2(max_abs2(max_abs2(bits, raw[p].x), raw[p].y), raw[p].z), raw[p].w);
+  bits = max(bits & 0xFFFFu, bits >> 16);
+  const bool odd = __any_sync(0xffffffffu, bits >= (DT == 1 ? 0x7F80u : 0x7C00u));
+  a = h2f<DT>((uint16_t)bits);
+  if (odd) {  // a value that is not finite: the others' maximum
+    a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[i]) ? fabsf(x[i]) : 0.0f);
+    for (int p = 0; p < PASSES; ++p) {
+      float x[8];
+      unpack8<DT>(raw[p], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[i]) ? fabsf(x[i]) : 0.0f);
+    }
   }
   const int t0 = w0 / g.blk * g.blk;  // the warp's block
   float* scales = (kv ? vs : ks) + g.scale(b, h, 0) + w0 / g.blk;
@@ -178,9 +199,14 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
   for (int p = 0; p < PASSES; ++p) {
     const int t = w0 + p * RPP + row;
     if (t < len || t >= end) continue;
-    float x[8];
-    unpack8<DT>(raw[p], x);
-    *reinterpret_cast<uint2*>(codes + g.row(b, h, t)) = kv8_encode8(x, inv);
+    uint2* to = reinterpret_cast<uint2*>(codes + g.row(b, h, t));
+    if (odd) {
+      float x[8];
+      unpack8<DT>(raw[p], x);
+      *to = kv8_encode8(x, inv);
+    } else {
+      *to = kv8_encode8_finite<DT>(raw[p], inv);
+    }
   }
   if (t0 < len && s != was) {
     const float ratio = was / s;
@@ -366,6 +392,12 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
   return h;
+}
+// Two fp16 values -> two E4M3 codes, as e4m3x2.
+__device__ __forceinline__ uint32_t f16_e4m3x2(__half2 h) {
+  uint16_t out;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(out) : "r"(*reinterpret_cast<uint32_t*>(&h)));
+  return out;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -806,7 +838,8 @@ __device__ __forceinline__ uint32_t kv8_key(float w) {
 }
 
 constexpr int kKv8SelThreads = 1024, kKv8SelBins = 2048;
-constexpr int kKv8SelKeep = 16;  // tokens a thread holds in registers
+constexpr int kKv8SelCluster = 8;  // CTAs that share a head's tokens, at most
+constexpr int kKv8SelKeep = 16;    // tokens a thread holds in registers
 
 // kept[b, h, i], i < min(len, budget): the tokens that stay, ascending: the
 // first `sink`, the last `recent`, and the heaviest of the others, ties to
@@ -820,9 +853,9 @@ template <bool REG>
 __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
     const float* __restrict__ weight, Kv8Geom g, const int32_t* __restrict__ seq_len, int budget,
     int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ len_out, int cl) {
-  __shared__ uint32_t hist[2][kKv8SelBins];
+  __shared__ __align__(8) uint32_t hist[2][kKv8SelBins];
   __shared__ int s_gt[32], s_eq[32], s_warp[32];
-  __shared__ float s_count[2];  // of this CTA, as bits
+  __shared__ __align__(8) uint32_t s_count[2];  // of this CTA
   __shared__ uint32_t s_prefix;
   __shared__ int s_rem, s_done;
   const int rank = blockIdx.x % cl, h = blockIdx.x / cl, b = blockIdx.y;
@@ -841,13 +874,16 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
   const int steps = (int)ceil_div(len, cl * kKv8SelThreads);  // of 32 tokens a warp
   const int from = (int)min((int64_t)len, ((int64_t)rank * 32 + warp) * 32 * steps);
   const int to = (int)min((int64_t)len, (int64_t)from + 32 * steps);
+  // Keys of this thread's tokens: all ones for a protected one (no number's
+  // key is), 0 (nor is that) behind the stretch.
+  auto load = [&](int t) {
+    const uint32_t k = kv8_key(__ldg(w + min(t, len - 1)));
+    return t >= to ? 0u : t < lo || t >= hi ? 0xFFFFFFFFu : k;
+  };
   uint32_t key[REG ? kKv8SelKeep : 1];
   if constexpr (REG) {
 #pragma unroll
-    for (int i = 0; i < kKv8SelKeep; ++i) {
-      const int t = from + 32 * i + lane;
-      key[i] = i < steps && t < to ? kv8_key(__ldg(w + t)) : 0u;
-    }
+    for (int i = 0; i < kKv8SelKeep; ++i) key[i] = load(from + 32 * i + lane);
   }
   // f(token, key) for this thread's tokens, 32 consecutive ones a warp
   auto each = [&](auto f) {
@@ -859,20 +895,18 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
       for (int i = 0; i < steps; i += 8) {
         uint32_t k8[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int t = from + 32 * (i + j) + lane;
-          k8[j] = i + j < steps && t < to ? kv8_key(__ldg(w + t)) : 0u;
-        }
+        for (int j = 0; j < 8; ++j) k8[j] = load(from + 32 * (i + j) + lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i + j < steps) f(from + 32 * (i + j) + lane, k8[j]);
+        for (int j = 0; j < 8; ++j) f(from + 32 * (i + j) + lane, k8[j]);
       }
     }
   };
   int rem = budget - sink - recent;
   uint32_t prefix = 0, pmask = 0;
+  bool all = false;  // of the keys at the threshold
   if (rem == 0) {
-    prefix = pmask = 0xFFFFFFFFu;  // no key of a number is all ones: none is taken
+    prefix = 0xFFFFFFFEu;  // above every number
+    pmask = 0xFFFFFFFFu;
   } else {
     for (int i = tid; i < 2 * kKv8SelBins; i += kKv8SelThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
@@ -881,20 +915,26 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
       uint32_t* mine = hist[pass & 1];
       each([&](int t, uint32_t k) {
-        if (t >= lo && t < hi && t < to && (k & pmask) == prefix)
+        if (k - 1u < 0xFFFFFFFEu && (k & pmask) == prefix)
           atomicAdd(&mine[(k >> shift) & mask], 1u);
       });
       if (cl > 1)
         cluster_sync();
       else
         __syncthreads();
-      // bins from the top, two a thread
+      // bins from the top, two a thread: top - 1, top
       const int top = kKv8SelBins - 1 - 2 * tid;
-      uint32_t c0 = mine[top], c1 = mine[top - 1];
-      for (int r = 1; r < cl; ++r) {
-        const float* theirs = reinterpret_cast<const float*>(mine);
-        c0 += __float_as_uint(ld_cluster(theirs + top, (rank + r) % cl));
-        c1 += __float_as_uint(ld_cluster(theirs + top - 1, (rank + r) % cl));
+      uint2 theirs[kKv8SelCluster];
+#pragma unroll
+      for (int r = 0; r < kKv8SelCluster; ++r)
+        theirs[r] = r == rank  ? *reinterpret_cast<const uint2*>(mine + top - 1)
+                    : r < cl ? ld_cluster2(mine + top - 1, r)
+                             : make_uint2(0, 0);
+      uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+      for (int r = 0; r < kKv8SelCluster; ++r) {
+        c0 += theirs[r].y;
+        c1 += theirs[r].x;
       }
       int upto = (int)(c0 + c1);
 #pragma unroll
@@ -904,8 +944,7 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
       }
       if (lane == 31) s_warp[warp] = upto;
       __syncthreads();
-      int before = 0;
-      for (int i = 0; i < warp; ++i) before += s_warp[i];
+      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
       upto += before;
       const int above0 = upto - (int)(c0 + c1), above1 = above0 + (int)c0;
       if (above0 < rem && rem <= upto) {  // one thread
@@ -922,54 +961,54 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
       prefix = s_prefix;
       rem = s_rem;
       pmask |= mask << shift;
-      if (s_done) break;  // the whole bucket is taken: the lower bits decide nothing
+      all = s_done;
+      if (all) break;  // the whole bucket is taken: the lower bits decide nothing
     }
   }
   // A token stays if protected, above the threshold, or one of the first
   // `rem` at it.
-  auto look = [&](int t, uint32_t k, bool& gt, bool& eq) {
-    const bool in = t < to, free = t >= lo && t < hi;
-    gt = in && (!free || (k & pmask) > prefix);
-    eq = in && free && (k & pmask) == prefix;
-  };
+  if (all) {
+    --prefix;  // the threshold itself is above this one
+    pmask = 0xFFFFFFFFu;
+    rem = 0;
+  }
   int ngt = 0, neq = 0;
   each([&](int t, uint32_t k) {
-    bool gt, eq;
-    look(t, k, gt, eq);
-    ngt += __popc(__ballot_sync(0xffffffffu, gt));
-    neq += __popc(__ballot_sync(0xffffffffu, eq));
+    ngt += __popc(__ballot_sync(0xffffffffu, (k & pmask) > prefix));
+    if (!all) neq += __popc(__ballot_sync(0xffffffffu, (k & pmask) == prefix));
   });
   if (lane == 0) {
     s_gt[warp] = ngt;
     s_eq[warp] = neq;
   }
   __syncthreads();
-  int gt0 = 0, eq0 = 0;
+  int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
   if (cl > 1) {
-    int all_gt = 0, all_eq = 0;
-    for (int i = 0; i < 32; ++i) {
-      all_gt += s_gt[i];
-      all_eq += s_eq[i];
-    }
-    if (tid == 0) {
-      s_count[0] = __int_as_float(all_gt);
-      s_count[1] = __int_as_float(all_eq);
+    if (warp == 0) {
+      const uint32_t gt = __reduce_add_sync(0xffffffffu, (uint32_t)s_gt[lane]);
+      const uint32_t eq = __reduce_add_sync(0xffffffffu, (uint32_t)s_eq[lane]);
+      if (lane == 0) {
+        s_count[0] = gt;
+        s_count[1] = eq;
+      }
     }
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      gt0 += __float_as_int(ld_cluster(s_count, r));
-      eq0 += __float_as_int(ld_cluster(s_count + 1, r));
-    }
-  }
-  for (int i = 0; i < warp; ++i) {
-    gt0 += s_gt[i];
-    eq0 += s_eq[i];
+    const uint2 c = lane < rank ? ld_cluster2(s_count, lane) : make_uint2(0, 0);
+    gt0 += (int)__reduce_add_sync(0xffffffffu, c.x);
+    eq0 += (int)__reduce_add_sync(0xffffffffu, c.y);
   }
   const unsigned below = (1u << lane) - 1u;
   each([&](int t, uint32_t k) {
-    bool gt, eq;
-    look(t, k, gt, eq);
-    const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+    const bool gt = (k & pmask) > prefix;
+    const unsigned mg = __ballot_sync(0xffffffffu, gt);
+    if (all) {
+      if (gt) out[gt0 + __popc(mg & below)] = t;
+      gt0 += __popc(mg);
+      return;
+    }
+    const bool eq = (k & pmask) == prefix;
+    const unsigned me = __ballot_sync(0xffffffffu, eq);
     const int e = eq0 + __popc(me & below);
     // survivors before this token: all above, and the first rem of the equal
     if (gt || (eq && e < rem)) out[gt0 + __popc(mg & below) + min(e, rem)] = t;
@@ -996,11 +1035,11 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
   const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 16 * (lane % TPR);
   const int n = min(g.len(seq_len, b), budget);
-  const int w0 = (int)blockIdx.x * TILE + warp * ROWS;
+  const int w0 = (int)blockIdx.x * TILE + warp * ROWS;  // this warp's rows
   if ((int)blockIdx.x * TILE >= n) return;
   const int wpb = g.blk > ROWS ? g.blk / ROWS : 1;
   const int64_t bh = (int64_t)b * g.Hkv + h;
-  const uint8_t* codes = (kv ? v : k) + c;
+  const uint8_t* codes = (kv ? v : k) + g.row(b, h, 0) + c;
   const float* scales = (kv ? vs : ks) + g.scale(b, h, 0);
   const int lb = 31 - __clz(g.blk);  // blk is a power of two
   pdl_wait();
@@ -1017,11 +1056,15 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
     w[p] = make_uint4(0, 0, 0, 0);
     s[p] = 0.0f;
     if (src[p] >= 0) {
-      w[p] = ldg_stream16(codes + g.row(b, h, src[p]));
+      w[p] = ldg_stream16(codes + src[p] * g.st);
       s[p] = __ldg(scales + (src[p] >> lb));
-      if (!kv && c == 0)
-        wo[bh * go.capacity + w0 + p * RPP + row] = __ldg(weight + bh * g.capacity + src[p]);
     }
+  }
+  if (!kv && c == 0) {
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+      if (src[p] >= 0)
+        wo[bh * go.capacity + w0 + p * RPP + row] = __ldg(weight + bh * g.capacity + src[p]);
   }
   float a = 0.0f;
 #pragma unroll
@@ -1042,21 +1085,27 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
   if (lane == 0) red[warp] = a;
   __syncthreads();
   if (w0 / g.blk * g.blk >= n) return;
-  const float so = kv8_scale(kv8_join(red, warp, wpb)), inv = kv8_inv(so);
+  const float so = kv8_scale(kv8_join(red, warp, wpb));
+  uint8_t* to = (kv ? vo : ko) + go.row(b, h, w0) + c;
+  // one product by the ratio of the scales, in two factors where it is no
+  // fp16 number (products below 2^-10 end as zeros, however far)
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    if (src[p] < 0) continue;
-    float x[8], y[8];
-    kv8_decode8(make_uint2(w[p].x, w[p].y), x);
-    kv8_decode8(make_uint2(w[p].z, w[p].w), y);
+    const int e = (int)(__float_as_uint(s[p]) >> 23) - (int)(__float_as_uint(so) >> 23);
+    const int e1 = max(-14, min(15, e)), e2 = max(-14, min(15, e - e1));
+    const __half2 f1 = __half2half2(__ushort_as_half((uint16_t)((e1 + 15) << 10)));
+    const __half2 f2 = __half2half2(__ushort_as_half((uint16_t)((e2 + 15) << 10)));
+    const uint32_t x[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+    uint32_t y[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] *= s[p];
-      y[e] *= s[p];
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = e4m3x2_f16(x[j]), hi = e4m3x2_f16(x[j] >> 16);
+      const __half2 l = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&lo), f1), f2);
+      const __half2 u = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&hi), f1), f2);
+      y[j] = f16_e4m3x2(l) | (f16_e4m3x2(u) << 16);
     }
-    const uint2 lo = kv8_encode8(x, inv), hi = kv8_encode8(y, inv);
-    *reinterpret_cast<uint4*>((kv ? vo : ko) + c + go.row(b, h, w0 + p * RPP + row)) =
-        make_uint4(lo.x, lo.y, hi.x, hi.y);
+    if (src[p] >= 0)
+      *reinterpret_cast<uint4*>(to + (p * RPP + row) * go.st) = make_uint4(y[0], y[1], y[2], y[3]);
   }
   if (lane == 0 && w0 % g.blk == 0) (kv ? vso : kso)[go.scale(b, h, w0 >> lb)] = so;
 }

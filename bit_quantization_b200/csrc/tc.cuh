@@ -388,6 +388,16 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
   return v;
 }
 
+// The two 32-bit words at this CTA's shared address p (8-byte aligned), in
+// the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint2 ld_cluster2(const uint32_t* p, int rank) {
+  uint32_t a;
+  uint2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // --------------------------------------------- shared-memory descriptors --
 
 enum SmemSwizzle : uint32_t { SW_NONE = 0, SW_128B = 2, SW_64B = 4, SW_32B = 6 };

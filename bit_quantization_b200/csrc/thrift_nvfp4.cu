@@ -700,7 +700,7 @@ cudaError_t kv8_select_launch(const float* weight, const Kv8Geom& g, const int32
                               int budget, int sink, int recent, int32_t* kept, int32_t* len_out,
                               cudaStream_t st) {
   int cl = 1;
-  while (cl < 8 && cl * 4 * kKv8SelThreads < g.capacity) cl *= 2;
+  while (cl < kKv8SelCluster && cl * 8 * kKv8SelThreads < g.capacity) cl *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(g.Hkv * cl, g.B);
   cfg.blockDim = dim3(kKv8SelThreads);
