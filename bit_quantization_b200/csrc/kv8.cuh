@@ -336,7 +336,6 @@ struct Kv8Dec {
   float scale;      // log2 e times the softmax scale
   float* part_o;    // [CTA][2][Gc][d], relative to the part's own maximum
   float* part_ml;   // [CTA][2][Gc][2] (maximum in log2 units, sum)
-  float* norm;      // [B, H, 2] (maximum, 1 / sum), or NULL
   float* scores;    // [B, Hkv, HG, capacity, Gc rounded to even] (log2 units), or NULL
   float* weight;
   uint16_t* out;
@@ -360,31 +359,20 @@ struct Kv8Plan {
   }
 };
 
-// Units of all sequences, and of those before sequence `upto`, by a whole CTA
-// (tmp: 2 ints a warp).
+// Units of all sequences, and of those before sequence `upto`, by every warp
+// for itself.
 template <int D>
-__device__ __forceinline__ int2 kv8_count(const Kv8Dec& p, int upto, int* tmp) {
+__device__ __forceinline__ int2 kv8_count(const Kv8Dec& p, int upto) {
   int all = 0, before = 0;
-  for (int b = threadIdx.x; b < p.g.B; b += blockDim.x) {
+#pragma unroll 4
+  for (int b = threadIdx.x & 31; b < p.g.B; b += 32) {
     const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
     all += n;
-    if (b < upto) before += n;
-  }
-  all = __reduce_add_sync(0xffffffffu, all);
-  before = __reduce_add_sync(0xffffffffu, before);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    tmp[2 * (threadIdx.x >> 5)] = all;
-    tmp[2 * (threadIdx.x >> 5) + 1] = before;
-  }
-  __syncthreads();
-  all = before = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    all += tmp[2 * w];
-    before += tmp[2 * w + 1];
+    before += b < upto ? n : 0;
   }
   const int per = p.g.Hkv * p.HG;
-  return make_int2(all * per, before * per);
+  return make_int2(per * __reduce_add_sync(0xffffffffu, all),
+                   per * __reduce_add_sync(0xffffffffu, before));
 }
 
 // Two E4M3 codes (the low or high half of c) -> two fp16 values (exact).
@@ -430,12 +418,11 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
   __shared__ float s_ml[kKv8DecWarps][8 * NT][2];
   __shared__ float s_qs[8 * NT];
   __shared__ __align__(16) uint16_t s_q[8 * NT][D];
-  __shared__ int tmp[2 * kKv8DecWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   const int Gp = (p.Gc + 1) & ~1;
   pdl_trigger();
   Kv8Plan plan;
-  plan.set(kv8_count<D>(p, 0, tmp).x, p.ctas);
+  plan.set(kv8_count<D>(p, 0).x, p.ctas);
   int u = plan.first(blockIdx.x);
   const int uend = plan.first(blockIdx.x + 1);
   if (u >= uend) return;
@@ -466,42 +453,6 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
     const int len = p.g.len(p.len, b), h = pair / p.HG, part = pair - h * p.HG;
     const int jn = min(n - j, uend - u), heads = min(p.Gc, p.G - part * p.Gc);
     const int64_t bh = (int64_t)b * p.H + h * p.G + part * p.Gc;  // first query head
-    // ---- q as fp16, two threads of a warp group a row
-    __syncthreads();
-    for (int r = warp; r < 8 * NT; r += kKv8DecWarps) {
-      float x[D / 32], top = 0.0f;
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        x[i] = r < heads ? h2f<DT>(__ldg(p.q + (bh + r) * D + 32 * i + lane)) : 0.0f;
-        top = fmaxf(top, fabsf(x[i]));
-        bad |= !finite_f(x[i]);
-      }
-      bad = __any_sync(0xffffffffu, bad);
-      float f = 1.0f, un = 1.0f;
-      if (DT == 1) {  // the largest value to [2^14, 2^15)
-        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23);
-        const int sh = min(max(141 - e, -126), 126);
-        f = __uint_as_float((uint32_t)(sh + 127) << 23);
-        un = __uint_as_float((uint32_t)(127 - sh) << 23);
-      }
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        s_q[r][32 * i + lane] = __half_as_ushort(__float2half_rn(bad ? 0.0f : x[i] * f));
-      if (lane == 0) s_qs[r] = bad ? NAN : un * p.scale;
-    }
-    __syncthreads();
-    uint2 qf[NT][KS];
-    float qs[NT][2];
-#pragma unroll
-    for (int a = 0; a < NT; ++a) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        qf[a][s] = *reinterpret_cast<const uint2*>(
-            &s_q[8 * a + gr][64 * (s >> 2) + 16 * t + 4 * (s & 3)]);
-      qs[a][0] = s_qs[8 * a + 2 * t];
-      qs[a][1] = s_qs[8 * a + 2 * t + 1];
-    }
     const uint8_t* kb = p.k + p.g.row(b, h, 0) + 16 * t;
     const uint8_t* vb = p.v + p.g.row(b, h, 0) + (D / 8) * gr;
     const float* ksp = p.ks + p.g.scale(b, h, 0);
@@ -547,6 +498,48 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
       }
     };
 
+    int t0 = j * UNIT + warp * STEP;
+    const int tend = min(len, (j + jn) * UNIT);
+    if (t0 < tend) {
+      load_k(t0);
+      load_v(t0);
+    }
+    // ---- q as fp16, a warp a row, while the first tokens arrive
+    __syncthreads();
+    for (int r = warp; r < 8 * NT; r += kKv8DecWarps) {
+      float x[D / 32], top = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        x[i] = r < heads ? h2f<DT>(__ldg(p.q + (bh + r) * D + 32 * i + lane)) : 0.0f;
+        top = fmaxf(top, fabsf(x[i]));
+        bad |= !finite_f(x[i]);
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      float f = 1.0f, un = 1.0f;
+      if (DT == 1) {  // the largest value to [2^14, 2^15)
+        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23);
+        const int sh = min(max(141 - e, -126), 126);
+        f = __uint_as_float((uint32_t)(sh + 127) << 23);
+        un = __uint_as_float((uint32_t)(127 - sh) << 23);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        s_q[r][32 * i + lane] = __half_as_ushort(__float2half_rn(bad ? 0.0f : x[i] * f));
+      if (lane == 0) s_qs[r] = bad ? NAN : un * p.scale;
+    }
+    __syncthreads();
+    uint2 qf[NT][KS];
+    float qs[NT][2];
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        qf[a][s] = *reinterpret_cast<const uint2*>(
+            &s_q[8 * a + gr][64 * (s >> 2) + 16 * t + 4 * (s & 3)]);
+      qs[a][0] = s_qs[8 * a + 2 * t];
+      qs[a][1] = s_qs[8 * a + 2 * t + 1];
+    }
     float o[NT][KS][4], m[NT][2], l[NT][2];
     float unit = 0.0f, umax = 0.0f;  // O is in units of `unit`
 #pragma unroll
@@ -557,12 +550,6 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
         for (int e = 0; e < 4; ++e) o[a][s][e] = 0.0f;
       m[a][0] = m[a][1] = -INFINITY;
       l[a][0] = l[a][1] = 0.0f;
-    }
-    int t0 = j * UNIT + warp * STEP;
-    const int tend = min(len, (j + jn) * UNIT);
-    if (t0 < tend) {
-      load_k(t0);
-      load_v(t0);
     }
     for (; t0 < tend; t0 += UNIT) {
       float sv[NG][NT][4];
@@ -736,95 +723,121 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
   }
 }
 
-// Parts of one (sequence, query head) merged, by 8 warps: out, lse, and what
-// the weights need.
+// What is left once every part is there, by role of the CTA.  The first B H:
+// the parts of one (sequence, query head) merged, by 8 warps: out and lse.
+// The others, for the weights: kKv8WeightTokens tokens of one (sequence, kv
+// head), weight += their probabilities summed over the group's heads, from the
+// scores that the pass over the keys has left.
+constexpr int kKv8WeightTokens = 2048;
+
 template <int DT, int D>
-__global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8Dec p) {
+__global__ void __launch_bounds__(256) kv8_finish_kernel(const Kv8Dec p) {
   constexpr int VEC = D / 32;
   __shared__ float s_o[8][D], s_m[8], s_l[8];
-  __shared__ int tmp[16];
-  const int hq = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = hq / p.G, part = (hq % p.G) / p.Gc, r = (hq % p.G) % p.Gc;
-  const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
-  const int2 count = kv8_count<D>(p, b, tmp);
+  __shared__ float2 s_norm[kKv8HeadGroup];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int merges = p.g.B * p.H;
+  if ((int)blockIdx.x < merges) {
+    const int b = blockIdx.x / p.H, hq = blockIdx.x % p.H;
+    const int h = hq / p.G, part = (hq % p.G) / p.Gc, r = (hq % p.G) % p.Gc;
+    const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
+    const int2 count = kv8_count<D>(p, b);
+    Kv8Plan plan;
+    plan.set(count.x, p.ctas);
+    const int u0 = count.y + (h * p.HG + part) * n;
+    const int a = n ? plan.owner(u0) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
+    pdl_wait();
+    float m = -INFINITY, l = 0.0f, o[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+#pragma unroll 4
+    for (int c = a + warp; c <= z; c += 8) {
+      const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);  // not its CTA's first part
+      const float* ml = p.part_ml + (slot * p.Gc + r) * 2;
+      const float mc = ml[0], lc = ml[1], mn = fmaxf(m, mc), ref = mn == -INFINITY ? 0.0f : mn;
+      const float x = exp2f(m - ref), y = exp2f(mc - ref);
+      const float* po = p.part_o + (slot * p.Gc + r) * D + VEC * lane;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = o[e] * x + po[e] * y;
+      l = l * x + lc * y;
+      m = mn;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s_o[warp][VEC * lane + e] = o[e];
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    __syncthreads();
+    if (tid >= D) return;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
+    const float ref = M == -INFINITY ? 0.0f : M;
+    float acc = 0.0f, L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float x = exp2f(s_m[w] - ref);
+      acc += s_o[w][tid] * x;
+      L += s_l[w] * x;
+    }
+    const int64_t bh = (int64_t)b * p.H + hq;
+    p.out[bh * D + tid] = f2h<DT>(n ? acc / L : 0.0f);
+    if (tid == 0) p.lse[bh] = n ? M * kLn2 + logf(L) : -INFINITY;
+    return;
+  }
+  const int chunks = (int)ceil_div(p.g.capacity, kKv8WeightTokens);
+  const int i = blockIdx.x - merges, pair = i / chunks, b = pair / p.g.Hkv, h = pair % p.g.Hkv;
+  const int len = p.g.len(p.len, b), first = (i % chunks) * kKv8WeightTokens;
+  if (first >= len) return;
+  const int n = (int)ceil_div(len, kv8_unit(D)), Gp = (p.Gc + 1) & ~1;
+  const int2 count = kv8_count<D>(p, b);
   Kv8Plan plan;
   plan.set(count.x, p.ctas);
-  const int u0 = count.y + (h * p.HG + part) * n;
-  const int a = n ? plan.owner(u0) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
+  float sum[kKv8WeightTokens / 256];
+#pragma unroll
+  for (int k = 0; k < kKv8WeightTokens / 256; ++k) sum[k] = 0.0f;
   pdl_wait();
-  float m = -INFINITY, l = 0.0f, o[VEC];
+  for (int part = 0; part < p.HG; ++part) {
+    const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
+    const int a = plan.owner(u0), z = plan.owner(u0 + n - 1);
+    __syncthreads();  // s_norm has been read
+    for (int r = warp; r < heads; r += 8) {  // maximum and 1 / sum of a head, its CTAs over the lanes
+      float M = -INFINITY, L = 0.0f;
+      for (int c = a + lane; c <= z; c += 32) {
+        const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.Gc + r) * 2);
+        const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.0f : mn;
+        L = L * exp2f(M - ref) + ml.y * exp2f(ml.x - ref);
+        M = mn;
+      }
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
-#pragma unroll 4
-  for (int c = a + warp; c <= z; c += 8) {
-    const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);  // not its CTA's first part
-    const float* ml = p.part_ml + (slot * p.Gc + r) * 2;
-    const float mc = ml[0], lc = ml[1], mn = fmaxf(m, mc), ref = mn == -INFINITY ? 0.0f : mn;
-    const float x = exp2f(m - ref), y = exp2f(mc - ref);
-    const float* po = p.part_o + (slot * p.Gc + r) * D + VEC * lane;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = o[e] * x + po[e] * y;
-    l = l * x + lc * y;
-    m = mn;
-  }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) s_o[warp][VEC * lane + e] = o[e];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  if (tid >= D) return;
-  float M = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
-  const float ref = M == -INFINITY ? 0.0f : M;
-  float acc = 0.0f, L = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float x = exp2f(s_m[w] - ref);
-    acc += s_o[w][tid] * x;
-    L += s_l[w] * x;
-  }
-  const int64_t bh = (int64_t)b * p.H + hq;
-  p.out[bh * D + tid] = f2h<DT>(n ? acc / L : 0.0f);
-  if (tid == 0) {
-    p.lse[bh] = n ? M * kLn2 + logf(L) : -INFINITY;
-    if (p.norm) {
-      p.norm[2 * bh] = M;
-      p.norm[2 * bh + 1] = 1.0f / L;
+      for (int o = 16; o >= 1; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+        const float mn = fmaxf(M, m2), ref = mn == -INFINITY ? 0.0f : mn;
+        L = L * exp2f(M - ref) + l2 * exp2f(m2 - ref);
+        M = mn;
+      }
+      if (lane == 0) s_norm[r] = make_float2(M, 1.0f / L);
     }
-  }
-}
-
-// weight[b, h, t] += the probabilities of token t, summed over the group's
-// heads, from the scores that the pass over the keys has left.
-constexpr int kKv8WeightTokens = 512;
-
-__global__ void __launch_bounds__(256) kv8_weight_kernel(const Kv8Dec p) {
-  const int h = blockIdx.y, b = blockIdx.z, len = p.g.len(p.len, b);
-  const int t0 = blockIdx.x * kKv8WeightTokens, Gp = (p.Gc + 1) & ~1;
-  if (t0 >= len) return;
-  pdl_wait();
-  for (int t = t0 + threadIdx.x; t < min(len, t0 + kKv8WeightTokens); t += 256) {
-    float sum = 0.0f;
-    for (int part = 0; part < p.HG; ++part) {
-      const int heads = min(p.Gc, p.G - part * p.Gc);
-      const float* s = p.scores +
-                       (((int64_t)(b * p.g.Hkv + h) * p.HG + part) * p.g.capacity + t) * Gp;
-      const float2* norm = reinterpret_cast<const float2*>(p.norm) + (int64_t)b * p.H + h * p.G +
-                           part * p.Gc;
+    __syncthreads();
+    const float* s = p.scores + ((int64_t)pair * p.HG + part) * p.g.capacity * Gp;
+#pragma unroll
+    for (int k = 0; k < kKv8WeightTokens / 256; ++k) {
+      const int t = first + 256 * k + tid;
+      if (t >= len) break;
       for (int r = 0; r < heads; r += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(s + r);
-        const float2 n0 = norm[r];
-        sum += exp2f(x.x - n0.x) * n0.y;
-        if (r + 1 < heads) {
-          const float2 n1 = norm[r + 1];
-          sum += exp2f(x.y - n1.x) * n1.y;
-        }
+        const float2 x = *reinterpret_cast<const float2*>(s + (int64_t)t * Gp + r);
+        sum[k] += exp2f(x.x - s_norm[r].x) * s_norm[r].y;
+        if (r + 1 < heads) sum[k] += exp2f(x.y - s_norm[r + 1].x) * s_norm[r + 1].y;
       }
     }
-    p.weight[((int64_t)b * p.g.Hkv + h) * p.g.capacity + t] += sum;
+  }
+  float* w = p.weight + (int64_t)pair * p.g.capacity;
+#pragma unroll
+  for (int k = 0; k < kKv8WeightTokens / 256; ++k) {
+    const int t = first + 256 * k + tid;
+    if (t < len) w[t] += sum[k];
   }
 }
 

@@ -729,7 +729,6 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
   };
   float* part_o = take((size_t)2 * kKv8MaxCtas * Gc * d);
   float* part_ml = take((size_t)2 * kKv8MaxCtas * Gc * 2);
-  float* norm = weights ? take((size_t)B * H * 2) : nullptr;
   float* scores =
       weights ? take((size_t)B * Hkv * HG * capacity * ((Gc + 1) & ~1)) : nullptr;
   if (p) {
@@ -739,7 +738,6 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
     p->Gc = Gc;
     p->part_o = part_o;
     p->part_ml = part_ml;
-    p->norm = norm;
     p->scores = scores;
   }
   return off;
@@ -753,11 +751,9 @@ thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
     kv8_decode_kernel<DT, D, 2><<<p.ctas, threads, 0, st>>>(p);
   else
     kv8_decode_kernel<DT, D, 1><<<p.ctas, threads, 0, st>>>(p);
-  cudaError_t e = launch_pdl(kv8_merge_kernel<DT, D>, dim3(p.H, p.g.B), 256, st, p);
-  if (e == cudaSuccess && p.weight)
-    e = launch_pdl(kv8_weight_kernel,
-                   dim3((unsigned)ceil_div(p.g.capacity, kKv8WeightTokens), p.g.Hkv, p.g.B), 256,
-                   st, p);
+  int64_t ctas = (int64_t)p.g.B * p.H;
+  if (p.weight) ctas += (int64_t)p.g.B * p.g.Hkv * ceil_div(p.g.capacity, kKv8WeightTokens);
+  const cudaError_t e = launch_pdl(kv8_finish_kernel<DT, D>, dim3((unsigned)ctas), 256, st, p);
   return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
