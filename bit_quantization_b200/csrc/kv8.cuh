@@ -316,7 +316,8 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
 // block's by an exact power of two.
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kKv8DecWarps = 4, kKv8DecCtas = 3;  // 168 registers a thread
+constexpr int kKv8DecWarps = 4;
+__host__ __device__ constexpr int kv8_dec_ctas(int nt) { return nt > 1 ? 2 : 3; }  // an SM
 constexpr int kKv8MaxCtas = 512;
 constexpr int kKv8HeadGroup = 16;                 // query heads in one pass over the cache
 
@@ -407,19 +408,22 @@ __device__ __forceinline__ uint2 ldg_stream8(const uint8_t* p) {
   return r;
 }
 
-// NT: heads of a part in eights.
+// NT: heads of a part in eights.  A part of 16 heads takes 230 registers a
+// thread: two CTAs an SM, the others three.
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
+__global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     kv8_decode_kernel(const Kv8Dec p) {
   constexpr int STEP = kv8_step(D), UNIT = kv8_unit(D), NG = STEP / 16;
-  constexpr int KS = D / 16;       // products along d
-  constexpr int VW = D / 32;       // words of a token's channels a thread holds
+  constexpr int KS = D / 16;  // products along d
+  constexpr int VW = D / 32;  // words of a token's channels a thread holds
+  constexpr int QR = 8 * NT / kKv8DecWarps;  // rows of q a warp prepares
   __shared__ float s_o[kKv8DecWarps][8 * NT][D + 1];
   __shared__ float s_ml[kKv8DecWarps][8 * NT][2];
   __shared__ float s_qs[8 * NT];
   __shared__ __align__(16) uint16_t s_q[8 * NT][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
-  const int Gp = (p.Gc + 1) & ~1;
+  const int Gp = (p.Gc + 1) & ~1, per = p.g.Hkv * p.HG;
+  const int lb = 31 - __clz(p.g.blk);  // blk is a power of two
   pdl_trigger();
   Kv8Plan plan;
   plan.set(kv8_count<D>(p, 0).x, p.ctas);
@@ -427,7 +431,6 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
   const int uend = plan.first(blockIdx.x + 1);
   if (u >= uend) return;
   // the sequence of unit u
-  const int per = p.g.Hkv * p.HG;
   int b = 0, n = 0, rel = u;
   for (int b0 = 0;; b0 += 32) {  // 32 sequences at a time
     const int mine = b0 + lane < p.g.B ? (int)ceil_div(p.g.len(p.len, b0 + lane), UNIT) : 0;
@@ -449,71 +452,89 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
     rel -= (before + n) * per;
   }
   int pair = rel / n, j = rel - pair * n;  // (kv head, part), unit of the sequence
-  for (int seg = 0; u < uend; ++seg) {
-    const int len = p.g.len(p.len, b), h = pair / p.HG, part = pair - h * p.HG;
-    const int jn = min(n - j, uend - u), heads = min(p.Gc, p.G - part * p.Gc);
-    const int64_t bh = (int64_t)b * p.H + h * p.G + part * p.Gc;  // first query head
-    const uint8_t* kb = p.k + p.g.row(b, h, 0) + 16 * t;
-    const uint8_t* vb = p.v + p.g.row(b, h, 0) + (D / 8) * gr;
-    const float* ksp = p.ks + p.g.scale(b, h, 0);
-    const float* vsp = p.vs + p.g.scale(b, h, 0);
-    const int lb = 31 - __clz(p.g.blk);  // blk is a power of two
-    float* sc = p.scores ? p.scores + (((int64_t)b * per + pair) * p.g.capacity) * Gp : nullptr;
 
-    uint4 kw[NG][2][D / 64];
-    uint32_t vw[NG][4][VW];
-    float ksc[NG], vsc[NG];
-    auto load_k = [&](int t0) {
+  // the stretch of one sequence, kv head and part that is at hand, the
+  // registers its tokens stream through, and its rows of q as they are
+  int len, jn, heads, t0, tend;
+  const uint8_t *kb, *vb;
+  const float *ksp, *vsp;
+  float* sc;
+  uint4 kw[NG][2][D / 64];
+  uint32_t vw[NG][4][VW];
+  float ksc[NG], vsc[NG];
+  uint32_t qraw[QR][D / 64];
+  auto load_k = [&](int first) {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
+    for (int i = 0; i < NG; ++i) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int tok = t0 + 16 * i + 8 * r + gr;
+      for (int r = 0; r < 2; ++r) {
+        const int tok = first + 16 * i + 8 * r + gr;
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-            kw[i][r][x] = tok < len ? ldg_stream16(kb + tok * p.g.st + 64 * x) : make_uint4(0, 0, 0, 0);
-        }
-        ksc[i] = t0 + 16 * i < len ? __ldg(ksp + ((t0 + 16 * i) >> lb)) : 1.0f;
+        for (int x = 0; x < D / 64; ++x)
+          kw[i][r][x] = tok < len ? ldg_stream16(kb + tok * p.g.st + 64 * x) : make_uint4(0, 0, 0, 0);
       }
-    };
-    auto load_v = [&](int t0) {
+      ksc[i] = first + 16 * i < len ? __ldg(ksp + ((first + 16 * i) >> lb)) : 1.0f;
+    }
+  };
+  auto load_v = [&](int first) {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
+    for (int i = 0; i < NG; ++i) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int tok = t0 + 16 * i + 2 * t + (r & 1) + 8 * (r >> 1);
-          if constexpr (D == 128) {
-            const uint4 w = tok < len ? ldg_stream16(vb + tok * p.g.st) : make_uint4(0, 0, 0, 0);
-            vw[i][r][0] = w.x;
-            vw[i][r][1] = w.y;
-            vw[i][r][2] = w.z;
-            vw[i][r][3] = w.w;
-          } else {
-            const uint2 w = tok < len ? ldg_stream8(vb + tok * p.g.st) : make_uint2(0, 0);
-            vw[i][r][0] = w.x;
-            vw[i][r][1] = w.y;
-          }
+      for (int r = 0; r < 4; ++r) {
+        const int tok = first + 16 * i + 2 * t + (r & 1) + 8 * (r >> 1);
+        if constexpr (D == 128) {
+          const uint4 w = tok < len ? ldg_stream16(vb + tok * p.g.st) : make_uint4(0, 0, 0, 0);
+          vw[i][r][0] = w.x;
+          vw[i][r][1] = w.y;
+          vw[i][r][2] = w.z;
+          vw[i][r][3] = w.w;
+        } else {
+          const uint2 w = tok < len ? ldg_stream8(vb + tok * p.g.st) : make_uint2(0, 0);
+          vw[i][r][0] = w.x;
+          vw[i][r][1] = w.y;
         }
-        vsc[i] = t0 + 16 * i < len ? __ldg(vsp + ((t0 + 16 * i) >> lb)) : 0.0f;
       }
-    };
-
-    int t0 = j * UNIT + warp * STEP;
-    const int tend = min(len, (j + jn) * UNIT);
+      vsc[i] = first + 16 * i < len ? __ldg(vsp + ((first + 16 * i) >> lb)) : 0.0f;
+    }
+  };
+  auto open = [&] {
+    const int h = pair / p.HG, part = pair - h * p.HG;
+    len = p.g.len(p.len, b);
+    jn = min(n - j, uend - u);
+    heads = min(p.Gc, p.G - part * p.Gc);
+    const uint16_t* q = p.q + ((int64_t)b * p.H + h * p.G + part * p.Gc) * D + lane * (D / 32);
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {  // channels lane * D / 32 on
+      const int r = warp + kKv8DecWarps * i;
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+        qraw[i][x] = r < heads ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D) + x) : 0u;
+    }
+    kb = p.k + p.g.row(b, h, 0) + 16 * t;
+    vb = p.v + p.g.row(b, h, 0) + (D / 8) * gr;
+    ksp = p.ks + p.g.scale(b, h, 0);
+    vsp = p.vs + p.g.scale(b, h, 0);
+    sc = p.scores ? p.scores + ((int64_t)b * per + pair) * p.g.capacity * Gp : nullptr;
+    t0 = j * UNIT + warp * STEP;
+    tend = min(len, (j + jn) * UNIT);
     if (t0 < tend) {
       load_k(t0);
       load_v(t0);
     }
+  };
+  open();
+  for (int seg = 0;; ++seg) {
     // ---- q as fp16, a warp a row, while the first tokens arrive
-    __syncthreads();
-    for (int r = warp; r < 8 * NT; r += kKv8DecWarps) {
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+      const int r = warp + kKv8DecWarps * i;
       float x[D / 32], top = 0.0f;
       bool bad = false;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        x[i] = r < heads ? h2f<DT>(__ldg(p.q + (bh + r) * D + 32 * i + lane)) : 0.0f;
-        top = fmaxf(top, fabsf(x[i]));
-        bad |= !finite_f(x[i]);
+      for (int e = 0; e < D / 32; ++e) {
+        x[e] = h2f<DT>((uint16_t)(e & 1 ? qraw[i][e >> 1] >> 16 : qraw[i][e >> 1] & 0xFFFFu));
+        top = fmaxf(top, fabsf(x[e]));
+        bad |= !finite_f(x[e]);
       }
       bad = __any_sync(0xffffffffu, bad);
       float f = 1.0f, un = 1.0f;
@@ -524,8 +545,9 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
         un = __uint_as_float((uint32_t)(127 - sh) << 23);
       }
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        s_q[r][32 * i + lane] = __half_as_ushort(__float2half_rn(bad ? 0.0f : x[i] * f));
+      for (int e = 0; e < D / 32; e += 2)
+        *reinterpret_cast<uint32_t*>(&s_q[r][lane * (D / 32) + e]) =
+            bad ? 0u : pack_f16(x[e] * f, x[e + 1] * f);
       if (lane == 0) s_qs[r] = bad ? NAN : un * p.scale;
     }
     __syncthreads();
@@ -669,7 +691,20 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
       }
       if (t0 + UNIT < tend) load_v(t0 + UNIT);
     }
-    // ---- the CTA's warps into one part
+    // ---- the next stretch's first tokens are on their way ...
+    const int done = heads;
+    u += jn;
+    j = 0;
+    const bool more = u < uend;
+    if (more) {
+      if (++pair == per) {
+        pair = 0;
+        do n = (int)ceil_div(p.g.len(p.len, ++b), UNIT);
+        while (n == 0);
+      }
+      open();
+    }
+    // ---- ... while the CTA's warps join this one's parts
 #pragma unroll
     for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -692,7 +727,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
     const int64_t slot = 2 * (int64_t)blockIdx.x + (seg > 0);
     float* po = p.part_o + slot * p.Gc * D;
     float* pm = p.part_ml + slot * p.Gc * 2;
-    for (int e = tid; e < heads * D; e += 32 * kKv8DecWarps) {
+    for (int e = tid; e < done * D; e += 32 * kKv8DecWarps) {
       const int r = e / D, c = e % D;
       float M = -INFINITY;
 #pragma unroll
@@ -702,7 +737,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
 #pragma unroll
       for (int w = 0; w < kKv8DecWarps; ++w) {
         // a warp without tokens has the maximum -inf and adds 0
-        const float x = exp2f(s_ml[w][r][0] - ref);
+        const float x = ex2(s_ml[w][r][0] - ref);
         acc += s_o[w][r][c] * x;
         L += s_ml[w][r][1] * x;
       }
@@ -712,14 +747,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kKv8DecCtas)
         pm[2 * r + 1] = L;
       }
     }
-    // next (kv head, part), or sequence
-    u += jn;
-    j = 0;
-    if (u < uend && ++pair == per) {
-      pair = 0;
-      do n = (int)ceil_div(p.g.len(p.len, ++b), UNIT);
-      while (n == 0);
-    }
+    if (!more) break;
   }
 }
 

@@ -745,7 +745,7 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
 
 template <int DT, int D>
 thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
-  p.ctas = std::min(kKv8MaxCtas, kKv8DecCtas * sm_count());
+  p.ctas = std::min(kKv8MaxCtas, kv8_dec_ctas(p.Gc > 8 ? 2 : 1) * sm_count());
   const int threads = 32 * kKv8DecWarps;
   if (p.Gc > 8)
     kv8_decode_kernel<DT, D, 2><<<p.ctas, threads, 0, st>>>(p);
