@@ -337,6 +337,7 @@ struct Kv8Dec {
   float scale;      // log2 e times the softmax scale
   float* part_o;    // [CTA][2][Gc][d], relative to the part's own maximum
   float* part_ml;   // [CTA][2][Gc][2] (maximum in log2 units, sum)
+  float2* norm;     // [B, H] (maximum, sum) where one CTA has had all, or NULL
   float* scores;    // [B, Hkv, HG, capacity, Gc rounded to even] (log2 units), or NULL
   float* weight;
   uint16_t* out;
@@ -346,6 +347,15 @@ struct Kv8Dec {
 
 // The work of a step is a row of units (sequence, kv head, part of the group,
 // kv8_unit tokens), dealt to the CTAs in equal runs whatever the lengths are.
+// Every stretch of tokens costs a CTA about one unit more than its tokens
+// (first loads, q, the join of the warps), so kKv8Head units without tokens
+// precede those of each (kv head, part): many short sequences would otherwise
+// fall to few CTAs.  A CTA has at most two stretches that others share, its
+// first and its last; one that is its own it finishes itself.
+#ifndef KV8HEAD
+#define KV8HEAD 1
+#endif
+constexpr int kKv8Head = KV8HEAD;
 struct Kv8Plan {
   int total, run, longer;  // the first `longer` CTAs take run + 1 units, the others run
   __device__ __forceinline__ void set(int units, int ctas) {
@@ -360,6 +370,13 @@ struct Kv8Plan {
   }
 };
 
+// Units of one (kv head, part) of a sequence.
+template <int D>
+__device__ __forceinline__ int kv8_units(const Kv8Dec& p, int b) {
+  const int len = p.g.len(p.len, b);
+  return len ? (int)ceil_div(len, kv8_unit(D)) + kKv8Head : 0;
+}
+
 // Units of all sequences, and of those before sequence `upto`, by every warp
 // for itself.
 template <int D>
@@ -367,7 +384,7 @@ __device__ __forceinline__ int2 kv8_count(const Kv8Dec& p, int upto) {
   int all = 0, before = 0;
 #pragma unroll 4
   for (int b = threadIdx.x & 31; b < p.g.B; b += 32) {
-    const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
+    const int n = kv8_units<D>(p, b);
     all += n;
     before += b < upto ? n : 0;
   }
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
   // the sequence of unit u
   int b = 0, n = 0, rel = u;
   for (int b0 = 0;; b0 += 32) {  // 32 sequences at a time
-    const int mine = b0 + lane < p.g.B ? (int)ceil_div(p.g.len(p.len, b0 + lane), UNIT) : 0;
+    const int mine = b0 + lane < p.g.B ? kv8_units<D>(p, b0 + lane) : 0;
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -451,11 +468,14 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     }
     rel -= (before + n) * per;
   }
-  int pair = rel / n, j = rel - pair * n;  // (kv head, part), unit of the sequence
+  int pair = rel / n, j = rel - pair * n;  // (kv head, part), unit of it
+  if (j + uend - u <= kKv8Head) return;    // no tokens
 
   // the stretch of one sequence, kv head and part that is at hand, the
   // registers its tokens stream through, and its rows of q as they are
   int len, jn, heads, t0, tend;
+  int64_t bh;  // the first query head
+  bool sole;   // nobody else has tokens of this sequence, kv head and part
   const uint8_t *kb, *vb;
   const float *ksp, *vsp;
   float* sc;
@@ -502,7 +522,9 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     len = p.g.len(p.len, b);
     jn = min(n - j, uend - u);
     heads = min(p.Gc, p.G - part * p.Gc);
-    const uint16_t* q = p.q + ((int64_t)b * p.H + h * p.G + part * p.Gc) * D + lane * (D / 32);
+    bh = (int64_t)b * p.H + h * p.G + part * p.Gc;
+    sole = j <= kKv8Head && j + jn == n;
+    const uint16_t* q = p.q + bh * D + lane * (D / 32);
 #pragma unroll
     for (int i = 0; i < QR; ++i) {  // channels lane * D / 32 on
       const int r = warp + kKv8DecWarps * i;
@@ -515,8 +537,8 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     ksp = p.ks + p.g.scale(b, h, 0);
     vsp = p.vs + p.g.scale(b, h, 0);
     sc = p.scores ? p.scores + ((int64_t)b * per + pair) * p.g.capacity * Gp : nullptr;
-    t0 = j * UNIT + warp * STEP;
-    tend = min(len, (j + jn) * UNIT);
+    t0 = max(0, j - kKv8Head) * UNIT + warp * STEP;
+    tend = min(len, (j + jn - kKv8Head) * UNIT);
     if (t0 < tend) {
       load_k(t0);
       load_v(t0);
@@ -693,13 +715,15 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     }
     // ---- the next stretch's first tokens are on their way ...
     const int done = heads;
+    const int64_t first_head = bh;
+    const bool mine = sole;
     u += jn;
     j = 0;
-    const bool more = u < uend;
+    const bool more = uend - u > kKv8Head;
     if (more) {
       if (++pair == per) {
         pair = 0;
-        do n = (int)ceil_div(p.g.len(p.len, ++b), UNIT);
+        do n = kv8_units<D>(p, ++b);
         while (n == 0);
       }
       open();
@@ -741,10 +765,18 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
         acc += s_o[w][r][c] * x;
         L += s_ml[w][r][1] * x;
       }
-      po[e] = acc;
-      if (c == 0) {
-        pm[2 * r] = M;
-        pm[2 * r + 1] = L;
+      if (mine) {
+        p.out[first_head * D + e] = f2h<DT>(acc / L);
+        if (c == 0) {
+          p.lse[first_head + r] = M * kLn2 + logf(L);
+          if (p.norm) p.norm[first_head + r] = make_float2(M, L);
+        }
+      } else {
+        po[e] = acc;
+        if (c == 0) {
+          pm[2 * r] = M;
+          pm[2 * r + 1] = L;
+        }
       }
     }
     if (!more) break;
@@ -768,13 +800,14 @@ __global__ void __launch_bounds__(256) kv8_finish_kernel(const Kv8Dec p) {
   if ((int)blockIdx.x < merges) {
     const int b = blockIdx.x / p.H, hq = blockIdx.x % p.H;
     const int h = hq / p.G, part = (hq % p.G) / p.Gc, r = (hq % p.G) % p.Gc;
-    const int n = (int)ceil_div(p.g.len(p.len, b), kv8_unit(D));
+    const int n = kv8_units<D>(p, b);
     const int2 count = kv8_count<D>(p, b);
     Kv8Plan plan;
     plan.set(count.x, p.ctas);
     const int u0 = count.y + (h * p.HG + part) * n;
-    const int a = n ? plan.owner(u0) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
+    const int a = n ? plan.owner(u0 + kKv8Head) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
     pdl_wait();
+    if (a == z) return;
     float m = -INFINITY, l = 0.0f, o[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
@@ -818,7 +851,7 @@ __global__ void __launch_bounds__(256) kv8_finish_kernel(const Kv8Dec p) {
   const int i = blockIdx.x - merges, pair = i / chunks, b = pair / p.g.Hkv, h = pair % p.g.Hkv;
   const int len = p.g.len(p.len, b), first = (i % chunks) * kKv8WeightTokens;
   if (first >= len) return;
-  const int n = (int)ceil_div(len, kv8_unit(D)), Gp = (p.Gc + 1) & ~1;
+  const int n = kv8_units<D>(p, b), Gp = (p.Gc + 1) & ~1;
   const int2 count = kv8_count<D>(p, b);
   Kv8Plan plan;
   plan.set(count.x, p.ctas);
@@ -828,11 +861,16 @@ __global__ void __launch_bounds__(256) kv8_finish_kernel(const Kv8Dec p) {
   pdl_wait();
   for (int part = 0; part < p.HG; ++part) {
     const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
-    const int a = plan.owner(u0), z = plan.owner(u0 + n - 1);
+    const int a = plan.owner(u0 + kKv8Head), z = plan.owner(u0 + n - 1);
     __syncthreads();  // s_norm has been read
     for (int r = warp; r < heads; r += 8) {  // maximum and 1 / sum of a head, its CTAs over the lanes
       float M = -INFINITY, L = 0.0f;
-      for (int c = a + lane; c <= z; c += 32) {
+      if (a == z && lane == 0) {
+        const float2 ml = p.norm[(int64_t)b * p.H + h * p.G + part * p.Gc + r];
+        M = ml.x;
+        L = ml.y;
+      }
+      for (int c = a + lane; c <= z && a < z; c += 32) {
         const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.Gc + r) * 2);
         const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.0f : mn;

@@ -729,6 +729,7 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
   };
   float* part_o = take((size_t)2 * kKv8MaxCtas * Gc * d);
   float* part_ml = take((size_t)2 * kKv8MaxCtas * Gc * 2);
+  float* norm = weights ? take((size_t)B * H * 2) : nullptr;
   float* scores =
       weights ? take((size_t)B * Hkv * HG * capacity * ((Gc + 1) & ~1)) : nullptr;
   if (p) {
@@ -738,6 +739,7 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
     p->Gc = Gc;
     p->part_o = part_o;
     p->part_ml = part_ml;
+    p->norm = reinterpret_cast<float2*>(norm);
     p->scores = scores;
   }
   return off;
@@ -1547,7 +1549,7 @@ thrift_status thrift_kv8_decode(const void* q, thrift_dtype dt, int B, int H, in
   if (ws_bytes < thrift_kv8_decode_workspace_size(B, H, Hkv, capacity, d, weight != nullptr))
     return THRIFT_ERR_ARG;
   // units of work are counted in 32 bits
-  if ((int64_t)B * H * ceil_div(capacity, kv8_unit(d)) >= (int64_t)1 << 30)
+  if ((int64_t)B * H * (ceil_div(capacity, kv8_unit(d)) + kKv8Head) >= (int64_t)1 << 30)
     return THRIFT_ERR_UNSUPPORTED;
   Kv8Dec p = {};
   kv8_decode_plan(B, H, Hkv, capacity, d, weight != nullptr, &p, static_cast<uint8_t*>(workspace));

@@ -183,6 +183,9 @@ DECODES = [
     ((1, 8, 6000, 128), 40, 64, "head", BF16, [5999]),
     ((40, 1, 260, 64), 5, 16, "pair", BF16, list(range(0, 260, 7))[:38] + [260, 259]),
     ((5, 4, 2100, 64), 16, 128, "token", FP16, [2048, 1, 0, 2100, 2049]),
+    # more (sequence, kv head) pairs than the machine takes at once
+    ((300, 8, 300, 64), 16, 32, "token", BF16, [(37 * i) % 301 for i in range(300)]),
+    ((160, 4, 700, 128), 36, 64, "head", FP16, [(97 * i) % 701 for i in range(160)]),
 ]
 
 
