@@ -342,7 +342,9 @@ struct Kv8Dec {
   float* weight;
   uint16_t* out;
   float* lse;
-  int ctas;
+  int ctas;     // of the pass over the cache
+  int weights;  // CTAs of the finish that add up weights
+  int lhc;      // log2 of the heads that a merging CTA of it takes: 0 .. 3
 };
 
 // The work of a step is a row of units (sequence, kv head, part of the group,
@@ -352,10 +354,7 @@ struct Kv8Dec {
 // precede those of each (kv head, part): many short sequences would otherwise
 // fall to few CTAs.  A CTA has at most two stretches that others share, its
 // first and its last; one that is its own it finishes itself.
-#ifndef KV8HEAD
-#define KV8HEAD 1
-#endif
-constexpr int kKv8Head = KV8HEAD;
+constexpr int kKv8Head = 1;
 struct Kv8Plan {
   int total, run, longer;  // the first `longer` CTAs take run + 1 units, the others run
   __device__ __forceinline__ void set(int units, int ctas) {
@@ -783,127 +782,153 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
   }
 }
 
-// What is left once every part is there, by role of the CTA.  The first B H:
-// the parts of one (sequence, query head) merged, by 8 warps: out and lse.
-// The others, for the weights: kKv8WeightTokens tokens of one (sequence, kv
+// What is left once every part is there, by role of the CTA.  The first
+// p.weights, for the weights: kKv8WeightTokens tokens of one (sequence, kv
 // head), weight += their probabilities summed over the group's heads, from the
-// scores that the pass over the keys has left.
+// scores that the pass over the keys has left.  The others: the parts of
+// 2^p.lhc query heads of one (sequence, kv head, part of the group) merged, the
+// 8 warps dealt to the heads: out and lse.
 constexpr int kKv8WeightTokens = 2048;
 
-template <int DT, int D>
-__global__ void __launch_bounds__(256) kv8_finish_kernel(const Kv8Dec p) {
+template <int DT, int D, bool WEIGHTS>
+__global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const Kv8Dec p) {
   constexpr int VEC = D / 32;
   __shared__ float s_o[8][D], s_m[8], s_l[8];
   __shared__ float2 s_norm[kKv8HeadGroup];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int merges = p.g.B * p.H;
-  if ((int)blockIdx.x < merges) {
-    const int b = blockIdx.x / p.H, hq = blockIdx.x % p.H;
-    const int h = hq / p.G, part = (hq % p.G) / p.Gc, r = (hq % p.G) % p.Gc;
-    const int n = kv8_units<D>(p, b);
+  if (WEIGHTS && (int)blockIdx.x < p.weights) {
+    const int chunks = (int)ceil_div(p.g.capacity, kKv8WeightTokens);
+    const int pair = (int)blockIdx.x / chunks, b = pair / p.g.Hkv, h = pair % p.g.Hkv;
+    const int len = p.g.len(p.len, b), first = ((int)blockIdx.x % chunks) * kKv8WeightTokens;
+    if (first >= len) return;
+    const int n = kv8_units<D>(p, b), Gp = (p.Gc + 1) & ~1;
     const int2 count = kv8_count<D>(p, b);
     Kv8Plan plan;
     plan.set(count.x, p.ctas);
-    const int u0 = count.y + (h * p.HG + part) * n;
-    const int a = n ? plan.owner(u0 + kKv8Head) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
+    float sum[kKv8WeightTokens / 256];
+#pragma unroll
+    for (int k = 0; k < kKv8WeightTokens / 256; ++k) sum[k] = 0.0f;
     pdl_wait();
-    if (a == z) return;
-    float m = -INFINITY, l = 0.0f, o[VEC];
+    for (int part = 0; part < p.HG; ++part) {
+      const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
+      const int a = plan.owner(u0 + kKv8Head), z = plan.owner(u0 + n - 1);
+      __syncthreads();  // s_norm has been read
+      for (int r = warp; r < heads; r += 8) {  // maximum and 1 / sum of a head, its CTAs over the lanes
+        float M = -INFINITY, L = 0.0f;
+        if (a == z && lane == 0) {
+          const float2 ml = p.norm[(int64_t)b * p.H + h * p.G + part * p.Gc + r];
+          M = ml.x;
+          L = ml.y;
+        }
+        for (int c = a + lane; c <= z && a < z; c += 32) {
+          const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);
+          const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.Gc + r) * 2);
+          const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.0f : mn;
+          L = L * exp2f(M - ref) + ml.y * exp2f(ml.x - ref);
+          M = mn;
+        }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int c = a + warp; c <= z; c += 8) {
-      const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);  // not its CTA's first part
-      const float* ml = p.part_ml + (slot * p.Gc + r) * 2;
-      const float mc = ml[0], lc = ml[1], mn = fmaxf(m, mc), ref = mn == -INFINITY ? 0.0f : mn;
-      const float x = exp2f(m - ref), y = exp2f(mc - ref);
-      const float* po = p.part_o + (slot * p.Gc + r) * D + VEC * lane;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) o[e] = o[e] * x + po[e] * y;
-      l = l * x + lc * y;
-      m = mn;
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s_o[warp][VEC * lane + e] = o[e];
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
-    }
-    __syncthreads();
-    if (tid >= D) return;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
-    const float ref = M == -INFINITY ? 0.0f : M;
-    float acc = 0.0f, L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float x = exp2f(s_m[w] - ref);
-      acc += s_o[w][tid] * x;
-      L += s_l[w] * x;
-    }
-    const int64_t bh = (int64_t)b * p.H + hq;
-    p.out[bh * D + tid] = f2h<DT>(n ? acc / L : 0.0f);
-    if (tid == 0) p.lse[bh] = n ? M * kLn2 + logf(L) : -INFINITY;
-    return;
-  }
-  const int chunks = (int)ceil_div(p.g.capacity, kKv8WeightTokens);
-  const int i = blockIdx.x - merges, pair = i / chunks, b = pair / p.g.Hkv, h = pair % p.g.Hkv;
-  const int len = p.g.len(p.len, b), first = (i % chunks) * kKv8WeightTokens;
-  if (first >= len) return;
-  const int n = kv8_units<D>(p, b), Gp = (p.Gc + 1) & ~1;
-  const int2 count = kv8_count<D>(p, b);
-  Kv8Plan plan;
-  plan.set(count.x, p.ctas);
-  float sum[kKv8WeightTokens / 256];
-#pragma unroll
-  for (int k = 0; k < kKv8WeightTokens / 256; ++k) sum[k] = 0.0f;
-  pdl_wait();
-  for (int part = 0; part < p.HG; ++part) {
-    const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
-    const int a = plan.owner(u0 + kKv8Head), z = plan.owner(u0 + n - 1);
-    __syncthreads();  // s_norm has been read
-    for (int r = warp; r < heads; r += 8) {  // maximum and 1 / sum of a head, its CTAs over the lanes
-      float M = -INFINITY, L = 0.0f;
-      if (a == z && lane == 0) {
-        const float2 ml = p.norm[(int64_t)b * p.H + h * p.G + part * p.Gc + r];
-        M = ml.x;
-        L = ml.y;
+        for (int o = 16; o >= 1; o >>= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+          const float mn = fmaxf(M, m2), ref = mn == -INFINITY ? 0.0f : mn;
+          L = L * exp2f(M - ref) + l2 * exp2f(m2 - ref);
+          M = mn;
+        }
+        if (lane == 0) s_norm[r] = make_float2(M, 1.0f / L);
       }
-      for (int c = a + lane; c <= z && a < z; c += 32) {
-        const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.Gc + r) * 2);
-        const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.0f : mn;
-        L = L * exp2f(M - ref) + ml.y * exp2f(ml.x - ref);
-        M = mn;
-      }
+      __syncthreads();
+      const float* s = p.scores + (((int64_t)pair * p.HG + part) * p.g.capacity + first + tid) * Gp;
+      for (int r = 0; r < heads; r += 2) {
+        const float2 n0 = s_norm[r], n1 = r + 1 < heads ? s_norm[r + 1] : make_float2(0.0f, 0.0f);
+        float2 x[kKv8WeightTokens / 256];
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
-        const float mn = fmaxf(M, m2), ref = mn == -INFINITY ? 0.0f : mn;
-        L = L * exp2f(M - ref) + l2 * exp2f(m2 - ref);
-        M = mn;
+        for (int k = 0; k < kKv8WeightTokens / 256; ++k)
+          x[k] = first + 256 * k + tid < len
+                     ? *reinterpret_cast<const float2*>(s + (int64_t)256 * k * Gp + r)
+                     : make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int k = 0; k < kKv8WeightTokens / 256; ++k) {
+          sum[k] = fmaf(exp2f(x[k].x - n0.x), n0.y, sum[k]);
+          if (r + 1 < heads) sum[k] = fmaf(exp2f(x[k].y - n1.x), n1.y, sum[k]);
+        }
       }
-      if (lane == 0) s_norm[r] = make_float2(M, 1.0f / L);
     }
-    __syncthreads();
-    const float* s = p.scores + ((int64_t)pair * p.HG + part) * p.g.capacity * Gp;
+    float* w = p.weight + (int64_t)pair * p.g.capacity;
 #pragma unroll
     for (int k = 0; k < kKv8WeightTokens / 256; ++k) {
       const int t = first + 256 * k + tid;
-      if (t >= len) break;
-      for (int r = 0; r < heads; r += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(s + (int64_t)t * Gp + r);
-        sum[k] += exp2f(x.x - s_norm[r].x) * s_norm[r].y;
-        if (r + 1 < heads) sum[k] += exp2f(x.y - s_norm[r + 1].x) * s_norm[r + 1].y;
+      if (t < len) w[t] += sum[k];
+    }
+    return;
+  }
+  const int groups = (p.Gc + (1 << p.lhc) - 1) >> p.lhc, per = p.g.Hkv * p.HG;
+  const int i = blockIdx.x - (WEIGHTS ? p.weights : 0), b = i / groups / per, pair = i / groups % per;
+  const int r0 = i % groups << p.lhc;  // the first of its heads in the part
+  const int heads = min(1 << p.lhc, min(p.Gc, p.G - pair % p.HG * p.Gc) - r0);
+  const int64_t bh = (int64_t)b * p.H + pair / p.HG * p.G + pair % p.HG * p.Gc + r0;
+  const int n = kv8_units<D>(p, b);
+  const int2 count = kv8_count<D>(p, b);
+  Kv8Plan plan;
+  plan.set(count.x, p.ctas);
+  const int u0 = count.y + pair * n;
+  const int a = n ? plan.owner(u0 + kKv8Head) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
+  const int split = 8 >> p.lhc, r = warp >> (3 - p.lhc);  // this warp's head
+  pdl_wait();
+  if (a == z || heads <= 0) return;
+  float m = -INFINITY, l = 0.0f, o[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+  constexpr int BATCH = 4;  // parts whose loads are in flight together
+  for (int c0 = a + (warp & (split - 1)); c0 <= z && r < heads; c0 += BATCH * split) {
+    float2 ml[BATCH];
+    float po[BATCH][VEC];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int c = c0 + k * split;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) po[k][e] = 0.0f;
+      if (c <= z) {
+        const int64_t slot = 2 * (int64_t)c + (plan.first(c) < u0);  // not its CTA's first stretch
+        const int64_t at = slot * p.Gc + r0 + r;
+        ml[k] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + VEC * lane + e);
+          po[k][e] = v.x;
+          po[k][e + 1] = v.y;
+        }
       }
     }
-  }
-  float* w = p.weight + (int64_t)pair * p.g.capacity;
 #pragma unroll
-  for (int k = 0; k < kKv8WeightTokens / 256; ++k) {
-    const int t = first + 256 * k + tid;
-    if (t < len) w[t] += sum[k];
+    for (int k = 0; k < BATCH; ++k) {
+      const float mn = fmaxf(m, ml[k].x), ref = mn == -INFINITY ? 0.0f : mn;
+      const float x = exp2f(m - ref), y = exp2f(ml[k].x - ref);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = o[e] * x + po[k][e] * y;
+      l = l * x + ml[k].y * y;
+      m = mn;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) s_o[warp][VEC * lane + e] = o[e];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  for (int e = tid; e < heads * D; e += 256) {
+    const int w0 = e / D * split, c = e % D;
+    float M = -INFINITY, acc = 0.0f, L = 0.0f;
+    for (int w = w0; w < w0 + split; ++w) M = fmaxf(M, s_m[w]);
+    const float ref = M == -INFINITY ? 0.0f : M;
+    for (int w = w0; w < w0 + split; ++w) {
+      const float x = exp2f(s_m[w] - ref);
+      acc += s_o[w][c] * x;
+      L += s_l[w] * x;
+    }
+    p.out[bh * D + e] = f2h<DT>(n ? acc / L : 0.0f);
+    if (c == 0) p.lse[bh + e / D] = n ? M * kLn2 + logf(L) : -INFINITY;
   }
 }
 

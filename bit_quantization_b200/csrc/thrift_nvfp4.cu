@@ -753,9 +753,13 @@ thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
     kv8_decode_kernel<DT, D, 2><<<p.ctas, threads, 0, st>>>(p);
   else
     kv8_decode_kernel<DT, D, 1><<<p.ctas, threads, 0, st>>>(p);
-  int64_t ctas = (int64_t)p.g.B * p.H;
-  if (p.weight) ctas += (int64_t)p.g.B * p.g.Hkv * ceil_div(p.g.capacity, kKv8WeightTokens);
-  const cudaError_t e = launch_pdl(kv8_finish_kernel<DT, D>, dim3((unsigned)ctas), 256, st, p);
+  // few heads have many parts each: a CTA a head; many have few: warps share
+  p.lhc = 0;
+  while (p.lhc < 3 && (1 << p.lhc) < p.Gc && p.g.B * p.H >> p.lhc > 4 * sm_count()) ++p.lhc;
+  p.weights = p.weight ? (int)(p.g.B * p.g.Hkv * ceil_div(p.g.capacity, kKv8WeightTokens)) : 0;
+  const int64_t merges = p.g.B * p.g.Hkv * p.HG * ceil_div(p.Gc, 1 << p.lhc);
+  const auto finish = p.weights ? kv8_finish_kernel<DT, D, true> : kv8_finish_kernel<DT, D, false>;
+  const cudaError_t e = launch_pdl(finish, dim3((unsigned)(p.weights + merges)), 256, st, p);
   return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
