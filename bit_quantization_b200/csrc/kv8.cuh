@@ -98,6 +98,8 @@ __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
 
 // ----------------------------------------------------------------- layout --
 
+constexpr int64_t kKv8MaxRow = 1 << 24;  // bytes from a token to the next, less than
+
 // Codes of one cache tensor: byte (b, h, t, c) at b sb + h sh + t st + c.
 struct Kv8Geom {
   int B, Hkv, capacity, blk, nblk;  // nblk = ceil(capacity / blk)
@@ -398,6 +400,13 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
   return h;
 }
+// The same of both halves of c.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
+}
 // Two fp16 values -> two E4M3 codes, as e4m3x2.
 __device__ __forceinline__ uint32_t f16_e4m3x2(__half2 h) {
   uint16_t out;
@@ -482,39 +491,69 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
   uint32_t vw[NG][4][VW];
   float ksc[NG], vsc[NG];
   uint32_t qraw[QR][D / 64];
+  // addresses: the sequence's and step's part is the warp's, a thread adds 32 bits
+  const uint32_t st = (uint32_t)p.g.st, koff = gr * st + 16 * t, voff = 2 * t * st + (D / 8) * gr;
   auto load_k = [&](int first) {
+    const uint8_t* base = kb + (int64_t)first * p.g.st;
+    if (first + STEP <= len) {
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
+      for (int i = 0; i < NG; ++i)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int tok = first + 16 * i + 8 * r + gr;
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          kw[i][r][x] = tok < len ? ldg_stream16(kb + tok * p.g.st + 64 * x) : make_uint4(0, 0, 0, 0);
-      }
-      ksc[i] = first + 16 * i < len ? __ldg(ksp + ((first + 16 * i) >> lb)) : 1.0f;
+          for (int x = 0; x < D / 64; ++x)
+            kw[i][r][x] = ldg_stream16(base + (koff + (16 * i + 8 * r) * st + 64 * x));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            kw[i][r][x] = make_uint4(0, 0, 0, 0);
+            if (first + 16 * i + 8 * r + gr < len)
+              kw[i][r][x] = ldg_stream16(base + (koff + (16 * i + 8 * r) * st + 64 * x));
+          }
     }
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      ksc[i] = first + 16 * i < len ? __ldg(ksp + ((first + 16 * i) >> lb)) : 1.0f;
   };
   auto load_v = [&](int first) {
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = first + 16 * i + 2 * t + (r & 1) + 8 * (r >> 1);
-        if constexpr (D == 128) {
-          const uint4 w = tok < len ? ldg_stream16(vb + tok * p.g.st) : make_uint4(0, 0, 0, 0);
-          vw[i][r][0] = w.x;
-          vw[i][r][1] = w.y;
-          vw[i][r][2] = w.z;
-          vw[i][r][3] = w.w;
-        } else {
-          const uint2 w = tok < len ? ldg_stream8(vb + tok * p.g.st) : make_uint2(0, 0);
-          vw[i][r][0] = w.x;
-          vw[i][r][1] = w.y;
-        }
+    const uint8_t* base = vb + (int64_t)first * p.g.st;
+    auto one = [&](uint32_t (&w)[VW], uint32_t off) {
+      if constexpr (D == 128) {
+        const uint4 x = ldg_stream16(base + off);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
+      } else {
+        const uint2 x = ldg_stream8(base + off);
+        w[0] = x.x;
+        w[1] = x.y;
       }
-      vsc[i] = first + 16 * i < len ? __ldg(vsp + ((first + 16 * i) >> lb)) : 0.0f;
+    };
+    if (first + STEP <= len) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          one(vw[i][r], voff + (16 * i + (r & 1) + 8 * (r >> 1)) * st);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int tok = 16 * i + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+          for (int x = 0; x < VW; ++x) vw[i][r][x] = 0;
+          if (first + tok + 2 * t < len) one(vw[i][r], voff + tok * st);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      vsc[i] = first + 16 * i < len ? __ldg(vsp + ((first + 16 * i) >> lb)) : 0.0f;
   };
   auto open = [&] {
     const int h = pair / p.HG, part = pair - h * p.HG;
@@ -531,8 +570,8 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
       for (int x = 0; x < D / 64; ++x)
         qraw[i][x] = r < heads ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D) + x) : 0u;
     }
-    kb = p.k + p.g.row(b, h, 0) + 16 * t;
-    vb = p.v + p.g.row(b, h, 0) + (D / 8) * gr;
+    kb = p.k + p.g.row(b, h, 0);
+    vb = p.v + p.g.row(b, h, 0);
     ksp = p.ks + p.g.scale(b, h, 0);
     vsp = p.vs + p.g.scale(b, h, 0);
     sc = p.scores ? p.scores + ((int64_t)b * per + pair) * p.g.capacity * Gp : nullptr;
@@ -607,8 +646,9 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
           const uint4 A = kw[i][0][s >> 2], B = kw[i][1][s >> 2];
           const uint32_t wa = (s & 3) == 0 ? A.x : (s & 3) == 1 ? A.y : (s & 3) == 2 ? A.z : A.w;
           const uint32_t wb = (s & 3) == 0 ? B.x : (s & 3) == 1 ? B.y : (s & 3) == 2 ? B.z : B.w;
-          const uint32_t a0 = e4m3x2_f16(wa), a2 = e4m3x2_f16(wa >> 16);
-          const uint32_t a1 = e4m3x2_f16(wb), a3 = e4m3x2_f16(wb >> 16);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_f16(wa, a0, a2);
+          e4m3x4_f16(wb, a1, a3);
 #pragma unroll
           for (int a = 0; a < NT; ++a)
             mma_16816(sv[i][a], a0, a1, a2, a3, qf[a][s].x, qf[a][s].y);
@@ -616,10 +656,16 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sv[i][a][e] *= qs[a][e & 1] * ksc[i];
-            if (t0 + 16 * i + gr + 8 * (e >> 1) >= len) sv[i][a][e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e) sv[i][a][e] *= qs[a][e & 1] * ksc[i];
+      }
+      if (t0 + STEP > len) {
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t0 + 16 * i + gr + 8 * (e >> 1) >= len) sv[i][a][e] = -INFINITY;
       }
       if (t0 + UNIT < tend) load_k(t0 + UNIT);
       if (sc) {
@@ -667,9 +713,15 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
             for (int e = 0; e < 4; ++e) o[a][s][e] *= mx[a][e & 1];
         }
       }
+      float ref[NT][2];
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ref[a][e] = m[a][e] == -INFINITY ? 0.0f : m[a][e];
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        if (vsc[i] != unit && t0 + 16 * i < len) {
+        if (t0 + 16 * i >= len) break;
+        if (vsc[i] != unit) {
           umax = fmaxf(umax, vsc[i]);
           // a block 2^60 below the largest so far counts in that one's units
           const float nu = vsc[i] < umax * 0x1p-60f ? umax * 0x1p-60f : vsc[i];
@@ -682,17 +734,19 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[a][s][e] *= f;
         }
-        const float ratio = vsc[i] == unit ? 1.0f : vsc[i] / unit;
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
           float pr[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float ref = m[a][e & 1] == -INFINITY ? 0.0f : m[a][e & 1];
-            pr[e] = ex2(sv[i][a][e] - ref);
+            pr[e] = ex2(sv[i][a][e] - ref[a][e & 1]);
             l[a][e & 1] += pr[e];
-            pr[e] *= ratio;
+          }
+          if (vsc[i] != unit) {
+            const float ratio = vsc[i] / unit;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[e] *= ratio;
           }
           b0[a] = transpose_8x8(pack_f16(pr[0], pr[1]));
           b1[a] = transpose_8x8(pack_f16(pr[2], pr[3]));
@@ -703,8 +757,9 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
           for (int y = 0; y < 2; ++y) {
             const uint32_t lo = __byte_perm(vw[i][0][x], vw[i][1][x], y ? 0x7362 : 0x5140);
             const uint32_t hi = __byte_perm(vw[i][2][x], vw[i][3][x], y ? 0x7362 : 0x5140);
-            const uint32_t a0 = e4m3x2_f16(lo), a1 = e4m3x2_f16(lo >> 16);
-            const uint32_t a2 = e4m3x2_f16(hi), a3 = e4m3x2_f16(hi >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_f16(lo, a0, a1);
+            e4m3x4_f16(hi, a2, a3);
 #pragma unroll
             for (int a = 0; a < NT; ++a) mma_16816(o[a][2 * x + y], a0, a1, a2, a3, b0[a], b1[a]);
           }

@@ -648,6 +648,7 @@ bool kv8_strides_ok(int B, int Hkv, int d, int capacity, int64_t sb, int64_t sh,
   if (B > 1) dim[n++] = {sb, B};
   if (Hkv > 1) dim[n++] = {sh, Hkv};
   if (capacity > 1) dim[n++] = {st, capacity};
+  if (capacity > 1 && st >= kKv8MaxRow) return false;
   std::sort(dim, dim + n);
   int64_t span = d;
   for (int i = 0; i < n; ++i) {
@@ -659,7 +660,9 @@ bool kv8_strides_ok(int B, int Hkv, int d, int capacity, int64_t sb, int64_t sh,
 }
 
 Kv8Geom kv8_geom(int B, int Hkv, int blk, int capacity, int64_t sb, int64_t sh, int64_t st) {
-  return Kv8Geom{B, Hkv, capacity, blk, (int)ceil_div(capacity, blk), sb, sh, st};
+  // the stride of an axis of size 1 is never used
+  return Kv8Geom{B, Hkv, capacity, blk, (int)ceil_div(capacity, blk), B > 1 ? sb : 0,
+                 Hkv > 1 ? sh : 0, capacity > 1 ? st : 0};
 }
 
 bool ranges_meet(const void* a, int64_t an, const void* b, int64_t bn) {

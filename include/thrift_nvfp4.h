@@ -344,7 +344,7 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  *   k, v            E4M3 codes [B, Hkv, capacity, d], the d codes of a row
  *                   contiguous, the other axes in any order: stride_b,
  *                   stride_h, stride_t in bytes (multiples of 16, rows not
- *                   overlapping; the stride of an axis of size 1 is not
+ *                   overlapping, stride_t below 2^24; the stride of an axis of size 1 is not
  *                   read).  K and V have the same strides, 16-byte aligned.
  *   k_scale, v_scale  fp32 [B, Hkv, ceil(capacity / blk)]: one scale per block
  *                   of blk tokens; a code stands for e4m3(code) * scale.
