@@ -321,6 +321,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kKv8DecWarps = 4;
 __host__ __device__ constexpr int kv8_dec_ctas(int nt) { return nt > 1 ? 2 : 3; }  // an SM
 constexpr int kKv8MaxCtas = 512;
+// Up to this capacity, and while every (sequence, kv head) has an SM, a CTA of
+// 8 warps takes all of one (up to 8 heads): 500 of 1024 tokens take 8.4 us
+// against 8.9 for the split and its merge and a full cache 11.8 against 9.2,
+// but a call costs the host a launch (2.4 us) less.
+constexpr int kKv8SoleTokens = 1024, kKv8SoleWarps = 8;
 constexpr int kKv8HeadGroup = 16;                 // query heads in one pass over the cache
 
 // Tokens a warp takes at a time, and a CTA.
@@ -433,51 +438,74 @@ __device__ __forceinline__ uint2 ldg_stream8(const uint8_t* p) {
   return r;
 }
 
-// NT: heads of a part in eights.  A part of 16 heads takes 230 registers a
-// thread: two CTAs an SM, the others three.
-template <int DT, int D, int NT>
-__global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
+// NT: heads of a part in eights.  A part of 16 heads takes 250 registers a
+// thread: two CTAs of four warps an SM, the others three.
+//
+// SOLE: a CTA a (sequence, kv head, part), of W warps, and nothing left to
+// finish: for caches so short and so few of them that the second launch would
+// cost more than the split gains.
+template <int DT, int D, int NT, int W, bool SOLE>
+__global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
     kv8_decode_kernel(const Kv8Dec p) {
-  constexpr int STEP = kv8_step(D), UNIT = kv8_unit(D), NG = STEP / 16;
+  constexpr int STEP = kv8_step(D), UNIT = W * STEP, NG = STEP / 16;
   constexpr int KS = D / 16;  // products along d
   constexpr int VW = D / 32;  // words of a token's channels a thread holds
-  constexpr int QR = 8 * NT / kKv8DecWarps;  // rows of q a warp prepares
-  __shared__ float s_o[kKv8DecWarps][8 * NT][D + 1];
-  __shared__ float s_ml[kKv8DecWarps][8 * NT][2];
+  constexpr int QR = 8 * NT / W;  // rows of q a warp prepares
+  static_assert(SOLE || UNIT == kv8_unit(D), "units as planned");
+  __shared__ float s_o[W][8 * NT][D + 1];
+  __shared__ float s_ml[W][8 * NT][2];
   __shared__ float s_qs[8 * NT];
   __shared__ __align__(16) uint16_t s_q[8 * NT][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   const int Gp = (p.Gc + 1) & ~1, per = p.g.Hkv * p.HG;
   const int lb = 31 - __clz(p.g.blk);  // blk is a power of two
   pdl_trigger();
-  Kv8Plan plan;
-  plan.set(kv8_count<D>(p, 0).x, p.ctas);
-  int u = plan.first(blockIdx.x);
-  const int uend = plan.first(blockIdx.x + 1);
-  if (u >= uend) return;
-  // the sequence of unit u
-  int b = 0, n = 0, rel = u;
-  for (int b0 = 0;; b0 += 32) {  // 32 sequences at a time
-    const int mine = b0 + lane < p.g.B ? kv8_units<D>(p, b0 + lane) : 0;
-    int upto = mine;
+  int b, n, pair, j, u, uend;
+  if constexpr (SOLE) {
+    b = blockIdx.x / per;
+    pair = blockIdx.x - b * per;
+    n = (int)ceil_div(p.g.len(p.len, b), UNIT) + kKv8Head;
+    j = u = 0;
+    uend = n;
+    if (n == kKv8Head) {  // an empty sequence
+      const int part = pair % p.HG, empty = min(p.Gc, p.G - part * p.Gc);
+      const int64_t first = (int64_t)b * p.H + pair / p.HG * p.G + part * p.Gc;
+      for (int e = tid; e < empty * D; e += 32 * W) p.out[first * D + e] = 0;
+      if (tid < empty) p.lse[first + tid] = -INFINITY;
+      return;
+    }
+  } else {
+    Kv8Plan plan;
+    plan.set(kv8_count<D>(p, 0).x, p.ctas);
+    u = plan.first(blockIdx.x);
+    uend = plan.first(blockIdx.x + 1);
+    if (u >= uend) return;
+    int rel = u;
+    b = n = 0;
+    // the sequence of unit u
+    for (int b0 = 0;; b0 += 32) {  // 32 sequences at a time
+      const int mine = b0 + lane < p.g.B ? kv8_units<D>(p, b0 + lane) : 0;
+      int upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, upto * per > rel);
+      const int at = past ? __ffs(past) - 1 : 31;
+      const int before = __shfl_sync(0xffffffffu, upto - mine, at);
+      n = __shfl_sync(0xffffffffu, mine, at);
+      if (past || b0 + 32 >= p.g.B) {
+        b = b0 + at;
+        rel -= before * per;
+        break;
+      }
+      rel -= (before + n) * per;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, upto * per > rel);
-    const int at = past ? __ffs(past) - 1 : 31;
-    const int before = __shfl_sync(0xffffffffu, upto - mine, at);
-    n = __shfl_sync(0xffffffffu, mine, at);
-    if (past || b0 + 32 >= p.g.B) {
-      b = b0 + at;
-      rel -= before * per;
-      break;
-    }
-    rel -= (before + n) * per;
+    pair = rel / n;  // (kv head, part)
+    j = rel - pair * n;  // unit of it
+    if (j + uend - u <= kKv8Head) return;  // no tokens
   }
-  int pair = rel / n, j = rel - pair * n;  // (kv head, part), unit of it
-  if (j + uend - u <= kKv8Head) return;    // no tokens
 
   // the stretch of one sequence, kv head and part that is at hand, the
   // registers its tokens stream through, and its rows of q as they are
@@ -565,7 +593,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     const uint16_t* q = p.q + bh * D + lane * (D / 32);
 #pragma unroll
     for (int i = 0; i < QR; ++i) {  // channels lane * D / 32 on
-      const int r = warp + kKv8DecWarps * i;
+      const int r = warp + W * i;
 #pragma unroll
       for (int x = 0; x < D / 64; ++x)
         qraw[i][x] = r < heads ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D) + x) : 0u;
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     // ---- q as fp16, a warp a row, while the first tokens arrive
 #pragma unroll
     for (int i = 0; i < QR; ++i) {
-      const int r = warp + kKv8DecWarps * i;
+      const int r = warp + W * i;
       float x[D / 32], top = 0.0f;
       bool bad = false;
 #pragma unroll
@@ -773,7 +801,7 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     const bool mine = sole;
     u += jn;
     j = 0;
-    const bool more = uend - u > kKv8Head;
+    const bool more = !SOLE && uend - u > kKv8Head;
     if (more) {
       if (++pair == per) {
         pair = 0;
@@ -805,21 +833,21 @@ __global__ void __launch_bounds__(32 * kKv8DecWarps, kv8_dec_ctas(NT))
     const int64_t slot = 2 * (int64_t)blockIdx.x + (seg > 0);
     float* po = p.part_o + slot * p.Gc * D;
     float* pm = p.part_ml + slot * p.Gc * 2;
-    for (int e = tid; e < done * D; e += 32 * kKv8DecWarps) {
+    for (int e = tid; e < done * D; e += 32 * W) {
       const int r = e / D, c = e % D;
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kKv8DecWarps; ++w) M = fmaxf(M, s_ml[w][r][0]);
+      for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][r][0]);
       const float ref = M == -INFINITY ? 0.0f : M;
       float acc = 0.0f, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kKv8DecWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         // a warp without tokens has the maximum -inf and adds 0
         const float x = ex2(s_ml[w][r][0] - ref);
         acc += s_o[w][r][c] * x;
         L += s_ml[w][r][1] * x;
       }
-      if (mine) {
+      if (SOLE || mine) {
         p.out[first_head * D + e] = f2h<DT>(acc / L);
         if (c == 0) {
           p.lse[first_head + r] = M * kLn2 + logf(L);

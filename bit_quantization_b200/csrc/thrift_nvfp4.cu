@@ -750,12 +750,17 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
 
 template <int DT, int D>
 thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
-  p.ctas = std::min(kKv8MaxCtas, kv8_dec_ctas(p.Gc > 8 ? 2 : 1) * sm_count());
+  const int nt = p.Gc > 8 ? 2 : 1, pairs = p.g.B * p.g.Hkv * p.HG;
+  if (nt == 1 && !p.weight && p.g.capacity <= kKv8SoleTokens && pairs <= sm_count()) {
+    kv8_decode_kernel<DT, D, 1, kKv8SoleWarps, true><<<pairs, 32 * kKv8SoleWarps, 0, st>>>(p);
+    return launch_status();
+  }
+  p.ctas = std::min(kKv8MaxCtas, kv8_dec_ctas(nt) * sm_count());
   const int threads = 32 * kKv8DecWarps;
-  if (p.Gc > 8)
-    kv8_decode_kernel<DT, D, 2><<<p.ctas, threads, 0, st>>>(p);
+  if (nt > 1)
+    kv8_decode_kernel<DT, D, 2, kKv8DecWarps, false><<<p.ctas, threads, 0, st>>>(p);
   else
-    kv8_decode_kernel<DT, D, 1><<<p.ctas, threads, 0, st>>>(p);
+    kv8_decode_kernel<DT, D, 1, kKv8DecWarps, false><<<p.ctas, threads, 0, st>>>(p);
   // few heads have many parts each: a CTA a head; many have few: warps share
   p.lhc = 0;
   while (p.lhc < 3 && (1 << p.lhc) < p.Gc && p.g.B * p.H >> p.lhc > 4 * sm_count()) ++p.lhc;

@@ -622,7 +622,8 @@ def thrift_attn_decode(q, cache: DoubleKVCache, topk_frac=0.0, sink_blocks=0, re
 
 # ----------------------------------------------------------- 8-bit cache --
 
-_F8 = torch.float8_e4m3fn
+_F8, _F32, _I32, _U8 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.uint8
+_16BIT = {torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _same_device(first, *ts):
@@ -662,8 +663,7 @@ def _scratch(nbytes, index):
 
 def _own_bytes(workspace):
     """Checks a workspace of the caller's."""
-    if workspace is not None and (workspace.dtype is not torch.uint8 or
-                                  not workspace.is_contiguous()):
+    if workspace is not None and (workspace.dtype is not _U8 or not workspace.is_contiguous()):
         raise ThriftError("workspace must be contiguous uint8")
 
 
@@ -681,18 +681,22 @@ def _call(index, what, fn, *args):
 def _kv8_cache(k, v, k_scale, v_scale, blk, what=""):
     """Checks the four tensors of an 8-bit cache; returns B, Hkv, capacity, d
     and the codes' strides (batch, head, token) in bytes."""
-    if k.dim() != 4 or k.dtype is not _F8 or v.dtype is not _F8 or v.shape != k.shape:
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 4 or k.dtype is not _F8 or v.dtype is not _F8 or v.shape != shape:
         raise ThriftError(f"k{what}, v{what} must be {_F8} [B, Hkv, capacity, d] of one shape")
-    strides = k.stride()
-    if v.stride() != strides or strides[3] != 1:
+    sb, sh, st, last = strides
+    if last != 1 or v.stride() != strides:
         raise ThriftError(f"k{what}, v{what} must have one layout, the last axis contiguous")
-    B, Hkv, cap, d = k.shape
-    if min(B, Hkv, cap) < 1 or blk not in (16, 32, 64, 128) or d not in (64, 128):
+    B, Hkv, cap, d = shape
+    if blk not in (16, 32, 64, 128) or d not in (64, 128) or B < 1 or Hkv < 1 or cap < 1:
         raise ThriftError("the 8-bit cache supports blk 16, 32, 64, 128 and d 64, 128")
-    shape = (B, Hkv, -(-cap // blk))
-    _dense(k_scale, shape, torch.float32, "k_scale" + what)
-    _dense(v_scale, shape, torch.float32, "v_scale" + what)
-    return B, Hkv, cap, d, strides[:3]
+    of = (B, Hkv, (cap + blk - 1) // blk)
+    if k_scale.shape != of or v_scale.shape != of or k_scale.dtype is not _F32 or \
+            v_scale.dtype is not _F32 or not k_scale.is_contiguous() or \
+            not v_scale.is_contiguous():
+        _dense(k_scale, of, _F32, "k_scale" + what)
+        _dense(v_scale, of, _F32, "v_scale" + what)
+    return B, Hkv, cap, d, sb, sh, st
 
 
 def thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new=None, blk=64,
@@ -703,23 +707,27 @@ def thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new=Non
     contiguous), k_scale, v_scale (f32 [B, Hkv, ceil(capacity / blk)]).
     ``weight`` (f32 [B, Hkv, capacity]) is zeroed for the new tokens;
     ``new_len`` (int32 [B], may be ``cache_len``) receives the new lengths."""
-    B, Hkv, cap, d, st = _kv8_cache(k, v, k_scale, v_scale, blk)
-    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[0] != B or \
-            k_new.shape[2:] != (Hkv, d):
+    B, Hkv, cap, d, sb, sh, st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    shape = k_new.shape
+    if len(shape) != 4 or v_new.shape != shape or shape[0] != B or shape[2] != Hkv or shape[3] != d:
         raise ThriftError(f"k_new, v_new must both be [{B}, T, {Hkv}, {d}]")
-    if k_new.dtype != v_new.dtype:
-        raise ThriftError("k_new and v_new differ in dtype")
-    _vector(cache_len, B, torch.int32, "cache_len")
-    _vector(n_new, B, torch.int32, "n_new")
-    _vector(new_len, B, torch.int32, "new_len")
-    _vector(weight, B * Hkv * cap, torch.float32, "weight")
-    _dense(k_new, k_new.shape, k_new.dtype, "k_new")
-    _dense(v_new, v_new.shape, v_new.dtype, "v_new")
+    dt = _16BIT.get(k_new.dtype)
+    if dt is None or v_new.dtype is not k_new.dtype:
+        raise ThriftError("k_new and v_new must be of one 16-bit type")
+    if not (k_new.is_contiguous() and v_new.is_contiguous()):
+        raise ThriftError("k_new and v_new must be contiguous")
+    _vector(cache_len, B, _I32, "cache_len")
+    if n_new is not None:
+        _vector(n_new, B, _I32, "n_new")
+    if new_len is not None:
+        _vector(new_len, B, _I32, "new_len")
+    if weight is not None:
+        _vector(weight, B * Hkv * cap, _F32, "weight")
     index = _same_device(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new, weight, new_len)
     _call(index, "thrift_kv8_append", lib().thrift_kv8_append, k_new.data_ptr(), v_new.data_ptr(),
-          _dt(k_new), B, Hkv, d, blk, cap, *st, cache_len.data_ptr(), _ptr(n_new),
-          k_new.shape[1], k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-          _ptr(weight), _ptr(new_len), _raw_stream(index))
+          dt, B, Hkv, d, blk, cap, sb, sh, st, cache_len.data_ptr(), _ptr(n_new), shape[1],
+          k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(weight),
+          _ptr(new_len), _raw_stream(index))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -734,26 +742,32 @@ def thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk=64, scale=None, we
     ``scale`` defaults to 1/sqrt(d).  ``weight`` (f32 [B, Hkv, capacity])
     accumulates each token's probability, summed over the query heads of its
     kv head."""
-    B, Hkv, cap, d, st = _kv8_cache(k, v, k_scale, v_scale, blk)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % Hkv:
+    B, Hkv, cap, d, sb, sh, st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != d or shape[1] % Hkv:
         raise ThriftError(f"q must be [{B}, H (a multiple of {Hkv}), {d}]")
-    H = q.shape[1]
-    _dense(q, q.shape, q.dtype, "q")
-    _dense(out, q.shape, q.dtype, "out")
-    _dense(lse, (B, H), torch.float32, "lse")
-    _vector(seq_len, B, torch.int32, "seq_len")
-    _vector(weight, B * Hkv * cap, torch.float32, "weight")
-    _own_bytes(workspace)
+    H, dt = shape[1], _16BIT.get(q.dtype)
+    if dt is None or not q.is_contiguous():
+        raise ThriftError(f"q must be contiguous and of a 16-bit type, got {q.dtype}")
+    _vector(seq_len, B, _I32, "seq_len")
+    if weight is not None:
+        _vector(weight, B * Hkv * cap, _F32, "weight")
+    if out is not None:
+        _dense(out, shape, q.dtype, "out")
+    if lse is not None:
+        _dense(lse, (B, H), _F32, "lse")
+    if workspace is not None:
+        _own_bytes(workspace)
     index = _same_device(q, k, v, k_scale, v_scale, seq_len, weight, out, lse, workspace)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = q.new_empty((B, H), dtype=torch.float32)
+        lse = torch.empty_strided((B, H), (H, 1), dtype=_F32, device=q.device)
     if workspace is None:
         workspace = _scratch(kv8_decode_workspace_size(B, H, Hkv, cap, d, weight is not None),
                              index)
-    _call(index, "thrift_kv8_decode", lib().thrift_kv8_decode, q.data_ptr(), _dt(q), B, H, Hkv, d,
-          blk, cap, *st, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+    _call(index, "thrift_kv8_decode", lib().thrift_kv8_decode, q.data_ptr(), dt, B, H, Hkv, d,
+          blk, cap, sb, sh, st, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
           seq_len.data_ptr(), d ** -0.5 if scale is None else float(scale), _ptr(weight),
           out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
           _raw_stream(index))
@@ -771,8 +785,8 @@ def thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_o
     stays of each (sequence, kv head) when its tokens are cut to ``budget``:
     the first ``sink``, the last ``recent`` and the heaviest others by
     ``weight``, in their order; ``len_out`` = min(seq_len, budget)."""
-    B, Hkv, cap, d, st = _kv8_cache(k, v, k_scale, v_scale, blk)
-    Bo, Ho, cap_o, do, sto = _kv8_cache(k_out, v_out, k_scale_out, v_scale_out, blk, "_out")
+    B, Hkv, cap, d, *st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    Bo, Ho, cap_o, do, *sto = _kv8_cache(k_out, v_out, k_scale_out, v_scale_out, blk, "_out")
     if (Bo, Ho, do) != (B, Hkv, d):
         raise ThriftError("the two caches must agree in batch, heads and d")
     budget, recent, sink = int(budget), int(recent), int(sink)
@@ -864,18 +878,20 @@ def nvfp4_linear(x, codes, scales, tensor_scale, out=None, workspace=None):
     if x.dim() != 2 or codes.dim() != 2:
         raise ThriftError("x must be [M, K] and codes [N, K/2]")
     M, K = x.shape
-    N = codes.shape[0]
-    dt = _dt(x)
-    _dense(x, (M, K), x.dtype, "x")
-    _dense(codes, (N, K // 2), torch.uint8, "codes")
-    _dense(scales, (N, K // 16), torch.uint8, "scales")
-    _dense(out, (M, N), x.dtype, "out")
-    _own_bytes(workspace)
-    if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() < 1:
-        raise ThriftError("tensor_scale must be float32 with at least one element")
+    N, dt = codes.shape[0], _16BIT.get(x.dtype)
+    if dt is None or not x.is_contiguous():
+        raise ThriftError(f"x must be contiguous and of a 16-bit type, got {x.dtype}")
     if M > 64 or K == 0 or K % 32 or K > 1 << 19:
         raise ThriftError("nvfp4_linear supports at most 64 rows and K a multiple of 32 up to "
                           "524288")
+    _dense(codes, (N, K // 2), _U8, "codes")
+    _dense(scales, (N, K // 16), _U8, "scales")
+    if tensor_scale.dtype is not _F32 or tensor_scale.numel() < 1:
+        raise ThriftError("tensor_scale must be float32 with at least one element")
+    if out is not None:
+        _dense(out, (M, N), x.dtype, "out")
+    if workspace is not None:
+        _own_bytes(workspace)
     index = _same_device(x, codes, scales, tensor_scale, out, workspace)
     if out is None:
         out = x.new_empty((M, N))
