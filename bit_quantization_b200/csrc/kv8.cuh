@@ -149,10 +149,11 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
   __shared__ float red[kKv8Warps];
   const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 8 * (lane % TPR);
+  pdl_wait();
+  pdl_trigger();
   const int len = g.len(cache_len, b);
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
-  pdl_trigger();
   const int64_t tile0 = (int64_t)(len / g.blk) * g.blk + (int64_t)blockIdx.x * TILE;
   if (tile0 >= end || end == len) return;
   const int w0 = (int)tile0 + warp * ROWS;  // this warp's rows [w0, w0 + ROWS)
@@ -235,6 +236,8 @@ __global__ void __launch_bounds__(1024) kv8_append_step_kernel(
   constexpr int TPR = D / 8, RPP = 32 / TPR, PASSES = kKv8StepTokens / RPP;
   const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane / TPR, c = 8 * (lane % TPR);
+  pdl_wait();
+  pdl_trigger();
   const int len = min(g.capacity, max(0, cache_len[b]));
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
@@ -287,6 +290,7 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
                                    const int32_t* __restrict__ n_new, int32_t* new_len) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   pdl_wait();  // the append still reads cache_len
+  pdl_trigger();
   if (b >= g.B) return;
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int len = min(g.capacity, max(0, cache_len[b]));
@@ -459,7 +463,8 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   const int Gp = (p.Gc + 1) & ~1, per = p.g.Hkv * p.HG;
   const int lb = 31 - __clz(p.g.blk);  // blk is a power of two
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();  // what follows may read the lengths: nothing before this writes them now
   int b, n, pair, j, u, uend;
   if constexpr (SOLE) {
     b = blockIdx.x / per;
@@ -892,6 +897,7 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
 #pragma unroll
     for (int k = 0; k < kKv8WeightTokens / 256; ++k) sum[k] = 0.0f;
     pdl_wait();
+    pdl_trigger();
     for (int part = 0; part < p.HG; ++part) {
       const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
       const int a = plan.owner(u0 + kKv8Head), z = plan.owner(u0 + n - 1);
@@ -957,6 +963,7 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
   const int a = n ? plan.owner(u0 + kKv8Head) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
   const int split = 8 >> p.lhc, r = warp >> (3 - p.lhc);  // this warp's head
   pdl_wait();
+  pdl_trigger();
   if (a == z || heads <= 0) return;
   float m = -INFINITY, l = 0.0f, o[VEC];
 #pragma unroll
@@ -1047,11 +1054,12 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
   __shared__ int s_rem, s_done;
   const int rank = blockIdx.x % cl, h = blockIdx.x / cl, b = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
   const int len = g.len(seq_len, b);
   const int64_t bh = (int64_t)b * g.Hkv + h;
   const float* w = weight + bh * g.capacity;
   int32_t* out = kept + bh * budget;
-  pdl_trigger();
   if (blockIdx.x == 0 && tid == 0) len_out[b] = min(len, budget);
   if (len <= budget) {
     for (int t = rank * kKv8SelThreads + tid; t < len; t += cl * kKv8SelThreads) out[t] = t;
@@ -1230,6 +1238,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
   const float* scales = (kv ? vs : ks) + g.scale(b, h, 0);
   const int lb = 31 - __clz(g.blk);  // blk is a power of two
   pdl_wait();
+  pdl_trigger();
   int src[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {

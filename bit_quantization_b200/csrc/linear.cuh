@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinP
   __shared__ uint32_t s_max;
   __shared__ float s_red;
   const int m = blockIdx.x / cl, rank = blockIdx.x % cl, tid = threadIdx.x;
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();  // the products may fetch weights: nothing before this writes them now
   if (blockIdx.x == 0)
     for (int i = tid; i < kLinMaxCtas * 4; i += kLinDigitThreads) reinterpret_cast<uint32_t*>(p.ws)[i] = 0;
   if (tid == 0) s_max = 0;
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         q.next(chunks, ntiles);
       }
       pdl_wait();
+      pdl_trigger();
       for (int k = 0; k < ahead; ++k) {
         digits(k, u);
         u.next(chunks, ntiles);
@@ -343,19 +345,24 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
           w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(s) + i) << (16 * (i & 1));
       return make_uint4(w[0], w[1], w[2], w[3]);
     };
+    // four units' scales (mostly 64 neighbouring bytes of a row) are loaded
+    // together while the four before are stored
     constexpr int AHEAD = 4;
-    uint4 ring[AHEAD];
+    uint4 next[AHEAD], ring[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) ring[i] = load(i);
+    for (int i = 0; i < AHEAD; ++i) next[i] = load(i);
     bool ok = true;
     int sl = 0, par = 1;  // of the stage's previous use; none in the first round
     for (int k0 = 0; k0 < n && ok; k0 += AHEAD) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) ring[i] = next[i];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) next[i] = load(k0 + AHEAD + i);
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         const int k = k0 + i;
         if (k >= n || !ok) continue;
         const uint4 v = ring[i];
-        ring[i] = load(k + AHEAD);
         if (k >= L::STAGES)
           ok = __all_sync(0xffffffffu, mbar_wait(empty + sl, par, s_abort));
         if (!ok) continue;

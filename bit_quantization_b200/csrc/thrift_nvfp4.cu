@@ -134,18 +134,26 @@ void launch_amax(const void* x, int64_t n_blocks, int G, uint32_t* out, cudaStre
 // while the previous kernel of the stream finishes; it waits for it
 // (pdl_wait) before touching anything that kernel may write.
 template <class Kernel, class... Args>
-cudaError_t launch_pdl(Kernel kernel, dim3 grid, int threads, cudaStream_t st, Args... args) {
+cudaError_t launch_pdl_cluster(Kernel kernel, dim3 grid, int threads, int cluster, size_t smem,
+                               cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)cluster, 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_pdl(Kernel kernel, dim3 grid, int threads, cudaStream_t st, Args... args) {
+  return launch_pdl_cluster(kernel, grid, threads, 1, 0, st, args...);
 }
 
 // Quantiser workspace: from byte 256, the per-CTA maxima of the partial
@@ -678,23 +686,24 @@ thrift_status kv8_append_impl(const void* kn, const void* vn, const Kv8Geom& g, 
                               cudaStream_t st) {
   if (max_new <= kKv8StepTokens) {
     // measured at 64 sequences x 8 heads and one token: 3.2 us against 6.1
-    kv8_append_step_kernel<DT, D><<<g.B, 32 * std::min(32, 2 * g.Hkv), 0, st>>>(
+    const cudaError_t e = launch_pdl(
+        kv8_append_step_kernel<DT, D>, dim3(g.B), 32 * std::min(32, 2 * g.Hkv), st,
         static_cast<const uint16_t*>(kn), static_cast<const uint16_t*>(vn), g, max_new, cache_len,
         n_new, static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), ks, vs, weight, new_len);
-    return launch_status();
+    return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
   }
   const int tile = kv8_tile(g.blk);
   // from the start of the block that the first token joins
   const int tiles = (int)ceil_div((int64_t)max_new + g.blk - 1, tile);
   const auto kernel = tile > 64 ? kv8_append_kernel<DT, D, 128> : kv8_append_kernel<DT, D, 64>;
-  kernel<<<dim3(tiles, 2 * g.Hkv, g.B), kKv8Threads, 0, st>>>(
-      static_cast<const uint16_t*>(kn), static_cast<const uint16_t*>(vn), g, max_new, cache_len,
-      n_new, static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), ks, vs, weight);
-  if (new_len &&
-      launch_pdl(kv8_advance_kernel, dim3((unsigned)ceil_div(g.B, kThreads)), kThreads, st, g,
-                 max_new, cache_len, n_new, new_len) != cudaSuccess)
-    return THRIFT_ERR_CUDA;
-  return launch_status();
+  cudaError_t e = launch_pdl(
+      kernel, dim3(tiles, 2 * g.Hkv, g.B), kKv8Threads, st, static_cast<const uint16_t*>(kn),
+      static_cast<const uint16_t*>(vn), g, max_new, cache_len, n_new, static_cast<uint8_t*>(k),
+      static_cast<uint8_t*>(v), ks, vs, weight);
+  if (e == cudaSuccess && new_len)
+    e = launch_pdl(kv8_advance_kernel, dim3((unsigned)ceil_div(g.B, kThreads)), kThreads, st, g,
+                   max_new, cache_len, n_new, new_len);
+  return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
 // The survivors of every (sequence, kv head): CTAs of a cluster until a
@@ -704,20 +713,11 @@ cudaError_t kv8_select_launch(const float* weight, const Kv8Geom& g, const int32
                               cudaStream_t st) {
   int cl = 1;
   while (cl < kKv8SelCluster && cl * 8 * kKv8SelThreads < g.capacity) cl *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(g.Hkv * cl, g.B);
-  cfg.blockDim = dim3(kKv8SelThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)cl, 1, 1};
-  cfg.attrs = at;
-  cfg.numAttrs = cl > 1;
   const auto kernel = (int64_t)cl * kKv8SelThreads * kKv8SelKeep >= g.capacity
                           ? kv8_select_kernel<true>
                           : kv8_select_kernel<false>;
-  return cudaLaunchKernelEx(&cfg, kernel, weight, g, seq_len, budget, sink, recent, kept, len_out,
-                            cl);
+  return launch_pdl_cluster(kernel, dim3(g.Hkv * cl, g.B), kKv8SelThreads, cl, 0, st, weight, g,
+                            seq_len, budget, sink, recent, kept, len_out, cl);
 }
 
 // Parts and workspace of a decode step.  Returns the bytes.
@@ -752,22 +752,22 @@ template <int DT, int D>
 thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
   const int nt = p.Gc > 8 ? 2 : 1, pairs = p.g.B * p.g.Hkv * p.HG;
   if (nt == 1 && !p.weight && p.g.capacity <= kKv8SoleTokens && pairs <= sm_count()) {
-    kv8_decode_kernel<DT, D, 1, kKv8SoleWarps, true><<<pairs, 32 * kKv8SoleWarps, 0, st>>>(p);
-    return launch_status();
+    const cudaError_t e = launch_pdl(kv8_decode_kernel<DT, D, 1, kKv8SoleWarps, true>, dim3(pairs),
+                                     32 * kKv8SoleWarps, st, p);
+    return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
   }
   p.ctas = std::min(kKv8MaxCtas, kv8_dec_ctas(nt) * sm_count());
-  const int threads = 32 * kKv8DecWarps;
-  if (nt > 1)
-    kv8_decode_kernel<DT, D, 2, kKv8DecWarps, false><<<p.ctas, threads, 0, st>>>(p);
-  else
-    kv8_decode_kernel<DT, D, 1, kKv8DecWarps, false><<<p.ctas, threads, 0, st>>>(p);
+  const auto pass = nt > 1 ? kv8_decode_kernel<DT, D, 2, kKv8DecWarps, false>
+                           : kv8_decode_kernel<DT, D, 1, kKv8DecWarps, false>;
+  cudaError_t e = launch_pdl(pass, dim3(p.ctas), 32 * kKv8DecWarps, st, p);
+  if (e != cudaSuccess) return THRIFT_ERR_CUDA;
   // few heads have many parts each: a CTA a head; many have few: warps share
   p.lhc = 0;
   while (p.lhc < 3 && (1 << p.lhc) < p.Gc && p.g.B * p.H >> p.lhc > 4 * sm_count()) ++p.lhc;
   p.weights = p.weight ? (int)(p.g.B * p.g.Hkv * ceil_div(p.g.capacity, kKv8WeightTokens)) : 0;
   const int64_t merges = p.g.B * p.g.Hkv * p.HG * ceil_div(p.Gc, 1 << p.lhc);
   const auto finish = p.weights ? kv8_finish_kernel<DT, D, true> : kv8_finish_kernel<DT, D, false>;
-  const cudaError_t e = launch_pdl(finish, dim3((unsigned)(p.weights + merges)), 256, st, p);
+  e = launch_pdl(finish, dim3((unsigned)(p.weights + merges)), 256, st, p);
   return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
@@ -821,24 +821,11 @@ thrift_status linear_launch(LinParams p, const uint8_t* codes, cudaStream_t st) 
     return THRIFT_ERR_CUDA;
   int cl = 1;  // CTAs that share a row of x, 8 values a thread
   while (cl < 8 && cl * 8 * kLinDigitThreads < p.K) cl *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.M * cl);
-  cfg.blockDim = dim3(kLinDigitThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)cl, 1, 1};
-  cfg.attrs = at;
-  cfg.numAttrs = cl > 1;
-  if (cudaLaunchKernelEx(&cfg, lin_digits_kernel<DT>, p, cl) != cudaSuccess) return THRIFT_ERR_CUDA;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = L::SMEM;
-  at[0] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, map, p) == cudaSuccess ? THRIFT_OK : THRIFT_ERR_CUDA;
+  cudaError_t e = launch_pdl_cluster(lin_digits_kernel<DT>, dim3(p.M * cl), kLinDigitThreads, cl,
+                                     0, st, p, cl);
+  if (e == cudaSuccess)
+    e = launch_pdl_cluster(kernel, dim3(grid), kLinThreads, 1, L::SMEM, st, map, p);
+  return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();
 }
 
 template <int DT>
