@@ -15,6 +15,11 @@
 
 namespace thrift {
 
+// Every kernel here may be scheduled while the kernel before it in the stream
+// ends, and waits for it first of all.  Only one that another kernel of the
+// same call follows lets that one be scheduled early: what comes after a call
+// may read the call's results before it waits (the quantiser does).
+
 // ------------------------------------------------------------ conversions --
 
 // Smallest 2^e, e >= -120, with a <= 448 * 2^e = 1.75 * 2^(e + 8); a >= 0
@@ -143,14 +148,14 @@ template <int DT, int D, int TILE>
 __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
     const uint16_t* __restrict__ kn, const uint16_t* __restrict__ vn, Kv8Geom g, int max_new,
     const int32_t* __restrict__ cache_len, const int32_t* __restrict__ n_new, uint8_t* k,
-    uint8_t* v, float* ks, float* vs, float* __restrict__ weight) {
+    uint8_t* v, float* ks, float* vs, float* __restrict__ weight, bool more) {
   constexpr int TPR = D / 8, RPP = 32 / TPR;  // threads a row (8 values each), rows a pass
   constexpr int ROWS = TILE / kKv8Warps, PASSES = ROWS / RPP;
   __shared__ float red[kKv8Warps];
   const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 8 * (lane % TPR);
   pdl_wait();
-  pdl_trigger();
+  if (more) pdl_trigger();
   const int len = g.len(cache_len, b);
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
@@ -237,7 +242,6 @@ __global__ void __launch_bounds__(1024) kv8_append_step_kernel(
   const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane / TPR, c = 8 * (lane % TPR);
   pdl_wait();
-  pdl_trigger();
   const int len = min(g.capacity, max(0, cache_len[b]));
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
@@ -290,7 +294,6 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
                                    const int32_t* __restrict__ n_new, int32_t* new_len) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   pdl_wait();  // the append still reads cache_len
-  pdl_trigger();
   if (b >= g.B) return;
   const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
   const int len = min(g.capacity, max(0, cache_len[b]));
@@ -464,7 +467,8 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
   const int Gp = (p.Gc + 1) & ~1, per = p.g.Hkv * p.HG;
   const int lb = 31 - __clz(p.g.blk);  // blk is a power of two
   pdl_wait();
-  pdl_trigger();  // what follows may read the lengths: nothing before this writes them now
+  // the finish may read the lengths: nothing before this writes them now
+  if (!SOLE) pdl_trigger();
   int b, n, pair, j, u, uend;
   if constexpr (SOLE) {
     b = blockIdx.x / per;
@@ -897,7 +901,6 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
 #pragma unroll
     for (int k = 0; k < kKv8WeightTokens / 256; ++k) sum[k] = 0.0f;
     pdl_wait();
-    pdl_trigger();
     for (int part = 0; part < p.HG; ++part) {
       const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
       const int a = plan.owner(u0 + kKv8Head), z = plan.owner(u0 + n - 1);
@@ -963,7 +966,6 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
   const int a = n ? plan.owner(u0 + kKv8Head) : 0, z = n ? plan.owner(u0 + n - 1) : -1;
   const int split = 8 >> p.lhc, r = warp >> (3 - p.lhc);  // this warp's head
   pdl_wait();
-  pdl_trigger();
   if (a == z || heads <= 0) return;
   float m = -INFINITY, l = 0.0f, o[VEC];
 #pragma unroll
@@ -1238,7 +1240,6 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
   const float* scales = (kv ? vs : ks) + g.scale(b, h, 0);
   const int lb = 31 - __clz(g.blk);  // blk is a power of two
   pdl_wait();
-  pdl_trigger();
   int src[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {

@@ -264,7 +264,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         q.next(chunks, ntiles);
       }
       pdl_wait();
-      pdl_trigger();
       for (int k = 0; k < ahead; ++k) {
         digits(k, u);
         u.next(chunks, ntiles);

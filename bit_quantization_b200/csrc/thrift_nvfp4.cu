@@ -699,7 +699,7 @@ thrift_status kv8_append_impl(const void* kn, const void* vn, const Kv8Geom& g, 
   cudaError_t e = launch_pdl(
       kernel, dim3(tiles, 2 * g.Hkv, g.B), kKv8Threads, st, static_cast<const uint16_t*>(kn),
       static_cast<const uint16_t*>(vn), g, max_new, cache_len, n_new, static_cast<uint8_t*>(k),
-      static_cast<uint8_t*>(v), ks, vs, weight);
+      static_cast<uint8_t*>(v), ks, vs, weight, new_len != nullptr);
   if (e == cudaSuccess && new_len)
     e = launch_pdl(kv8_advance_kernel, dim3((unsigned)ceil_div(g.B, kThreads)), kThreads, st, g,
                    max_new, cache_len, n_new, new_len);

@@ -119,6 +119,33 @@ def test_linear_repeats_across_streams_and_graphs():
     assert ops.device_status() == ops.OK
 
 
+def test_results_are_complete_for_the_call_that_follows():
+    """The quantiser, whose first kernel reads its input as soon as it is
+    scheduled, right behind the attention (split and in one launch) and the
+    linear layer: the same codes as from their finished results."""
+    gen = torch.Generator().manual_seed(15)
+    args = _weights(4096, 4096, gen)
+    x = torch.randn((16, 4096), generator=gen).to(BF16).cuda()
+    caches = [ops.KV8Cache(B, 8, cap, d=128, blk=64) for B, cap in ((8, 8000), (2, 1000))]
+    qs = []
+    for c in caches:
+        B, _, cap, _ = c.k.shape
+        new = torch.randn((B, cap, 8, 128), generator=gen).to(BF16).cuda()
+        c.append(new, -new)
+        qs.append(torch.randn((B, 32, 128), generator=gen).to(BF16).cuda())
+    for i in range(20):
+        for call in [lambda: ops.nvfp4_linear(x, *args)] + [
+                lambda c=c, q=q: c.decode(q, accumulate=bool(i % 2))[0].view(-1, 128)
+                for c, q in zip(caches, qs)]:
+            torch.cuda.synchronize()
+            y = call()
+            got = ops.nvfp4_quantize(y)
+            torch.cuda.synchronize()
+            want = ops.nvfp4_quantize(y)
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+
+
 def test_linear_empty():
     x = torch.zeros((0, 64), dtype=BF16, device="cuda")
     codes = torch.zeros((5, 32), dtype=torch.uint8, device="cuda")
