@@ -92,39 +92,34 @@ __device__ __forceinline__ float2 e2m1x2_decode(uint32_t c) {
 
 // ----------------------------------------------------------------- digits --
 
-// One row of x: a cluster of CTAs finds its largest value, then every thread
-// writes the digits of 8 values, two threads the scale of a block of 16.
+// `parts` CTAs a row of x: each finds the row's largest value for itself (from
+// L2, which is quicker than asking the others), then every thread writes the
+// digits of 8 values, two threads the scale of a block of 16.
 template <int DT>
-__global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinParams p, int cl) {
+__global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinParams p, int parts) {
   __shared__ uint32_t s_max;
-  __shared__ float s_red;
-  const int m = blockIdx.x / cl, rank = blockIdx.x % cl, tid = threadIdx.x;
+  const int m = blockIdx.x / parts, rank = blockIdx.x % parts, tid = threadIdx.x;
+  if (tid == 0) s_max = 0;
   pdl_wait();
   pdl_trigger();  // the products may fetch weights: nothing before this writes them now
   if (blockIdx.x == 0)
-    for (int i = tid; i < kLinMaxCtas * 4; i += kLinDigitThreads) reinterpret_cast<uint32_t*>(p.ws)[i] = 0;
-  if (tid == 0) s_max = 0;
+    for (int i = tid; i < kLinMaxCtas * 4; i += kLinDigitThreads)
+      reinterpret_cast<uint32_t*>(p.ws)[i] = 0;
   __syncthreads();
   const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.K);
-  const int n8 = p.K / 8, first = rank * kLinDigitThreads + tid, step = cl * kLinDigitThreads;
+  const int n8 = p.K / 8, first = rank * kLinDigitThreads + tid, step = parts * kLinDigitThreads;
   uint32_t a = 0;  // bits of |x|: ordered, infinities and NaN on top
-  uint4 v = make_uint4(0, 0, 0, 0), head = v;  // head: the first, kept for the digits
-  for (int i = first; i < n8; i += step) {
-    v = __ldg(src + i);
-    if (i == first) head = v;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a = max(a, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+#pragma unroll 4
+  for (int i = tid; i < n8; i += kLinDigitThreads) {
+    const uint4 v = __ldg(src + i);
+    const uint32_t w = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    a = __vmaxu2(a, w);
   }
-  a = __reduce_max_sync(0xffffffffu, a);
+  a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
   if ((tid & 31) == 0) atomicMax(&s_max, a);
   __syncthreads();
   a = s_max;
-  if (cl > 1) {
-    if (tid == 0) s_red = __uint_as_float(s_max);
-    cluster_sync();
-    for (int k = 0; k < cl; ++k) a = max(a, __float_as_uint(ld_cluster(&s_red, k)));
-  }
   const bool finite = a < (DT == 1 ? 0x7F80u : 0x7C00u);
   // the largest value to [2^9, 2^10), in two factors: 2^135 is not an fp32 number
   const float top = h2f<DT>((uint16_t)a);
@@ -138,8 +133,8 @@ __global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinP
   uint8_t* img = p.ws + p.img + (int64_t)grp * p.chunks * lin_img(p.cols);
   // the last chunk is written to its end: its weights are zeros there, x too
   for (int i = first; i < p.chunks * (kLinChunk / 8); i += step) {
-    v = make_uint4(0, 0, 0, 0);
-    if (i < n8 && finite) v = i == first ? head : __ldg(src + i);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (i < n8 && finite) v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float x[8], top8 = 0.0f;
 #pragma unroll
@@ -171,7 +166,6 @@ __global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinP
       if (!(k8 & 1)) at[p.cols * 128 + sf_offset(col + d, k8 >> 1)] = (uint8_t)sf;
     }
   }
-  if (cl > 1) cluster_sync();  // nobody leaves while its maximum is read
 }
 
 // ---------------------------------------------------------------- product --
@@ -424,12 +418,11 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
 #pragma unroll
         for (int m = 0; m < ROWS; ++m)
           if (m < M) __stcg(mine + m * 128, v[m]);
-        __threadfence();
         __syncwarp();
         uint32_t before = 0;
-        if (lane == 0) before = atomicAdd(arrived + 4 * a + quarter, 1u);
+        if (lane == 0) before = atom_add_acq_rel(arrived + 4 * a + quarter, 1u);
         if (__shfl_sync(0xffffffffu, before, 0) != (uint32_t)(b - a)) continue;
-        __threadfence();
+        __syncwarp();  // what lane 0 has acquired is the warp's
         // in the order of the CTAs, the loads of BATCH of them together
         constexpr int BATCH = 16 / ROWS;
         const float* theirs = part + (int64_t)2 * a * ROWS * 128;

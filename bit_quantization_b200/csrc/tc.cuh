@@ -94,6 +94,18 @@ __device__ __forceinline__ bool spin_until_geq(const unsigned* word, unsigned ta
   }
 }
 
+// Adds to a global word, after everything the warp wrote before its last
+// __syncwarp is visible to the GPU, and before what follows reads: returns the
+// old value.
+__device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* word, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(word), "r"(v)
+               : "memory");
+  return old;
+}
+
 // Programmatic dependent launch.  pdl_wait: waits until the grid this one
 // depends on in its stream has completed and its memory operations are
 // visible (returns at once when there is none: a kernel launched without the

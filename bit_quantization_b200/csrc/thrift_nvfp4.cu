@@ -819,10 +819,8 @@ thrift_status linear_launch(LinParams p, const uint8_t* codes, cudaStream_t st) 
              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return THRIFT_ERR_CUDA;
-  int cl = 1;  // CTAs that share a row of x, 8 values a thread
-  while (cl < 8 && cl * 8 * kLinDigitThreads < p.K) cl *= 2;
-  cudaError_t e = launch_pdl_cluster(lin_digits_kernel<DT>, dim3(p.M * cl), kLinDigitThreads, cl,
-                                     0, st, p, cl);
+  const int parts = (int)std::min<int64_t>(ceil_div(p.K, 8 * kLinDigitThreads), 16);
+  cudaError_t e = launch_pdl(lin_digits_kernel<DT>, dim3(p.M * parts), kLinDigitThreads, st, p, parts);
   if (e == cudaSuccess)
     e = launch_pdl_cluster(kernel, dim3(grid), kLinThreads, 1, L::SMEM, st, map, p);
   return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();

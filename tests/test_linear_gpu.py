@@ -34,6 +34,7 @@ def _check(x, codes, scales, g, y):
     (1, 32, 1), (1, 64, 7), (2, 96, 128), (3, 256, 129), (1, 4096, 1024), (5, 2080, 300),
     (7, 1056, 1111), (8, 512, 2000), (16, 4096, 256), (15, 224, 513), (17, 320, 130),
     (33, 1024, 200), (64, 640, 384), (1, 16384, 257), (4, 14336, 128), (2, 4064, 5000),
+    (1, 65536, 33), (18, 24544, 260), (2, 524288, 3),
 ])
 def test_linear(M, K, N, dtype):
     gen = torch.Generator().manual_seed(M * 1000 + K + N)
