@@ -1035,7 +1035,6 @@ __device__ __forceinline__ uint32_t kv8_key(float w) {
 
 constexpr int kKv8SelThreads = 1024, kKv8SelBins = 2048;
 constexpr int kKv8SelCluster = 8;  // CTAs that share a head's tokens, at most
-constexpr int kKv8SelKeep = 16;    // tokens a thread holds in registers
 
 // kept[b, h, i], i < min(len, budget): the tokens that stay, ascending: the
 // first `sink`, the last `recent`, and the heaviest of the others, ties to
@@ -1043,9 +1042,9 @@ constexpr int kKv8SelKeep = 16;    // tokens a thread holds in registers
 // contiguous stretch of tokens: a radix select of 11, 11 and 10 bits over the
 // candidates' keys, whose histograms are added over distributed shared memory
 // (every CTA arrives at the same digit), then every warp writes the survivors
-// of its stretch behind those of the lower ones.  REG: the keys stay in
-// registers from one read; else every pass reads them again.
-template <bool REG>
+// of its stretch behind those of the lower ones.  KEEP: the tokens whose keys
+// a thread holds in registers from one read; 0: every pass reads them again.
+template <int KEEP>
 __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
     const float* __restrict__ weight, Kv8Geom g, const int32_t* __restrict__ seq_len, int budget,
     int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ len_out, int cl) {
@@ -1073,28 +1072,34 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
   const int to = (int)min((int64_t)len, (int64_t)from + 32 * steps);
   // Keys of this thread's tokens: all ones for a protected one (no number's
   // key is), 0 (nor is that) behind the stretch.
-  auto load = [&](int t) {
-    const uint32_t k = kv8_key(__ldg(w + min(t, len - 1)));
+  auto key_of = [&](int t, float x) {
+    const uint32_t k = kv8_key(x);
     return t >= to ? 0u : t < lo || t >= hi ? 0xFFFFFFFFu : k;
   };
-  uint32_t key[REG ? kKv8SelKeep : 1];
-  if constexpr (REG) {
+  uint32_t key[KEEP > 0 ? KEEP : 1];
+  if constexpr (KEEP > 0) {
+    float x[KEEP];  // every load is on its way before the first is waited for
 #pragma unroll
-    for (int i = 0; i < kKv8SelKeep; ++i) key[i] = load(from + 32 * i + lane);
+    for (int i = 0; i < KEEP; ++i) x[i] = __ldg(w + min(from + 32 * i + lane, len - 1));
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) key[i] = key_of(from + 32 * i + lane, x[i]);
   }
   // f(token, key) for this thread's tokens, 32 consecutive ones a warp
   auto each = [&](auto f) {
-    if constexpr (REG) {
+    if constexpr (KEEP > 0) {
 #pragma unroll
-      for (int i = 0; i < kKv8SelKeep; ++i)
+      for (int i = 0; i < KEEP; ++i)
         if (i < steps) f(from + 32 * i + lane, key[i]);
     } else {
       for (int i = 0; i < steps; i += 8) {
-        uint32_t k8[8];
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) k8[j] = load(from + 32 * (i + j) + lane);
+        for (int j = 0; j < 8; ++j) x[j] = __ldg(w + min(from + 32 * (i + j) + lane, len - 1));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f(from + 32 * (i + j) + lane, k8[j]);
+        for (int j = 0; j < 8; ++j) {
+          const int t = from + 32 * (i + j) + lane;
+          f(t, key_of(t, x[j]));
+        }
       }
     }
   };

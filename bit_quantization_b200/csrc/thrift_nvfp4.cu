@@ -713,9 +713,10 @@ cudaError_t kv8_select_launch(const float* weight, const Kv8Geom& g, const int32
                               cudaStream_t st) {
   int cl = 1;
   while (cl < kKv8SelCluster && cl * 8 * kKv8SelThreads < g.capacity) cl *= 2;
-  const auto kernel = (int64_t)cl * kKv8SelThreads * kKv8SelKeep >= g.capacity
-                          ? kv8_select_kernel<true>
-                          : kv8_select_kernel<false>;
+  const int64_t a_thread = ceil_div(g.capacity, (int64_t)cl * kKv8SelThreads);
+  const auto kernel = a_thread <= 8    ? kv8_select_kernel<8>
+                      : a_thread <= 16 ? kv8_select_kernel<16>
+                                       : kv8_select_kernel<0>;
   return launch_pdl_cluster(kernel, dim3(g.Hkv * cl, g.B), kKv8SelThreads, cl, 0, st, weight, g,
                             seq_len, budget, sink, recent, kept, len_out, cl);
 }
