@@ -1036,6 +1036,16 @@ __device__ __forceinline__ uint32_t kv8_key(float w) {
 constexpr int kKv8SelThreads = 1024, kKv8SelBins = 2048;
 constexpr int kKv8SelCluster = 8;  // CTAs that share a head's tokens, at most
 
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int warp_scan(int x) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((int)(threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+
 // kept[b, h, i], i < min(len, budget): the tokens that stay, ascending: the
 // first `sink`, the last `recent`, and the heaviest of the others, ties to
 // the lower token.  A cluster of CTAs per (kv head, sequence), a warp a
@@ -1048,8 +1058,9 @@ template <int KEEP>
 __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
     const float* __restrict__ weight, Kv8Geom g, const int32_t* __restrict__ seq_len, int budget,
     int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ len_out, int cl) {
-  __shared__ __align__(8) uint32_t hist[2][kKv8SelBins];
-  __shared__ int s_gt[32], s_eq[32], s_warp[32];
+  __shared__ uint32_t hist[2][kKv8SelBins];
+  __shared__ uint32_t coarse[2][64], s_theirs[64 * kKv8SelCluster];
+  __shared__ int s_gt[32], s_eq[32], s_bin, s_above;
   __shared__ __align__(8) uint32_t s_count[2];  // of this CTA
   __shared__ uint32_t s_prefix;
   __shared__ int s_rem, s_done;
@@ -1120,41 +1131,52 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
         if (k - 1u < 0xFFFFFFFEu && (k & pmask) == prefix)
           atomicAdd(&mine[(k >> shift) & mask], 1u);
       });
+      // sums of 32 bins, two a warp; then of all CTAs: the 64 sums to find the 32
+      // bins that hold the threshold, and those bins
+      __syncthreads();
+      uint32_t* sums = coarse[pass & 1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = __reduce_add_sync(0xffffffffu, mine[64 * warp + 32 * i + lane]);
+        if (lane == 0) sums[2 * warp + i] = x;
+      }
       if (cl > 1)
         cluster_sync();
       else
         __syncthreads();
-      // bins from the top, two a thread: top - 1, top
-      const int top = kKv8SelBins - 1 - 2 * tid;
-      uint2 theirs[kKv8SelCluster];
-#pragma unroll
-      for (int r = 0; r < kKv8SelCluster; ++r)
-        theirs[r] = r == rank  ? *reinterpret_cast<const uint2*>(mine + top - 1)
-                    : r < cl ? ld_cluster2(mine + top - 1, r)
-                             : make_uint2(0, 0);
-      uint32_t c0 = 0, c1 = 0;
-#pragma unroll
-      for (int r = 0; r < kKv8SelCluster; ++r) {
-        c0 += theirs[r].y;
-        c1 += theirs[r].x;
-      }
-      int upto = (int)(c0 + c1);
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      if (lane == 31) s_warp[warp] = upto;
+      auto theirs = [&](const uint32_t* at, int r) {
+        return r == rank ? *at : r < cl ? __float_as_uint(ld_cluster(reinterpret_cast<const float*>(at), r)) : 0u;
+      };
+      if (tid < 64 * kKv8SelCluster) s_theirs[tid] = theirs(sums + (tid & 63), tid >> 6);
       __syncthreads();
-      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
-      upto += before;
-      const int above0 = upto - (int)(c0 + c1), above1 = above0 + (int)c0;
-      if (above0 < rem && rem <= upto) {  // one thread
-        const bool first = rem <= above1;
-        const int n = (int)(first ? c0 : c1);
-        s_rem = rem - (first ? above0 : above1);
-        s_prefix = prefix | (uint32_t)(first ? top : top - 1) << shift;
-        s_done = n == s_rem;
+      if (warp == 0) {
+        const int top = 63 - 2 * lane;  // the lane's upper bin of the two
+        int c0 = 0, c1 = 0;
+#pragma unroll
+        for (int r = 0; r < kKv8SelCluster; ++r) {
+          c0 += (int)s_theirs[64 * r + top];
+          c1 += (int)s_theirs[64 * r + top - 1];
+        }
+        const int above0 = warp_scan(c0 + c1) - c0 - c1, above1 = above0 + c0;
+        if (above0 < rem && rem <= above1 + c1) {  // one lane
+          s_bin = rem <= above1 ? top : top - 1;
+          s_above = rem <= above1 ? above0 : above1;
+        }
+      }
+      __syncthreads();
+      const int bin0 = 32 * s_bin;
+      if (tid < 32 * kKv8SelCluster) s_theirs[tid] = theirs(mine + bin0 + (tid & 31), tid >> 5);
+      __syncthreads();
+      if (warp == 0) {
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < kKv8SelCluster; ++r) c += (int)s_theirs[32 * r + 31 - lane];
+        const int above = s_above + warp_scan(c) - c;
+        if (above < rem && rem <= above + c) {  // one lane
+          s_rem = rem - above;
+          s_prefix = prefix | (uint32_t)(bin0 + 31 - lane) << shift;
+          s_done = c == s_rem;
+        }
       }
       // the other buffer, free since every CTA of the cluster has come here
       if (pass == 1)

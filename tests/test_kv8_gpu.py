@@ -304,6 +304,9 @@ EVICTS = [
     ((1, 2, 3000, 64), 32, "token", [2999], 1, 0, 0, 33),
     ((1, 1, 5000, 64), 32, "head", [5000], 2500, 100, 4, 2500),
     ((2, 2, 70, 64), 16, "head", [70, 69], 1000, 3, 3, 70),
+    # weights shared by a cluster, and more than its registers hold
+    ((2, 1, 20000, 64), 32, "token", [20000, 11111], 9000, 64, 4, 9001),
+    ((1, 1, 140001, 64), 128, "head", [140001], 70000, 5, 3, 70000),
 ]
 
 
