@@ -1301,45 +1301,58 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
         wo[bh * go.capacity + w0 + p * RPP + row] = __ldg(weight + bh * g.capacity + src[p]);
   }
   float a = 0.0f;
+  uint32_t nan = 0;  // a bit of every byte that is a NaN
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const uint32_t x[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
     __half2 top = __float2half2_rn(0.0f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = e4m3x2_f16(x[j]), hi = e4m3x2_f16(x[j] >> 16);
-      top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&lo)));
-      top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&hi)));
+      const uint32_t m = x[j] & 0x7F7F7F7Fu;
+      nan |= (m + 0x01010101u) & 0x80808080u;
+      uint32_t lo, hi;
+      e4m3x4_f16(m, lo, hi);
+      top = __hmax2(top, *reinterpret_cast<const __half2*>(&lo));
+      top = __hmax2(top, *reinterpret_cast<const __half2*>(&hi));
     }
     const float2 f = __half22float2(top);
     const float y = fmaxf(f.x, f.y) * fabsf(s[p]);
     a = fmaxf(a, finite_f(y) ? y : 0.0f);
   }
+  const bool odd = __any_sync(0xffffffffu, nan != 0);
   a = warp_max(a);
   if (lane == 0) red[warp] = a;
   __syncthreads();
   if (w0 / g.blk * g.blk >= n) return;
   const float so = kv8_scale(kv8_join(red, warp, wpb));
   uint8_t* to = (kv ? vo : ko) + go.row(b, h, w0) + c;
-  // one product by the ratio of the scales, in two factors where it is no
-  // fp16 number (products below 2^-10 end as zeros, however far)
+  // Rows whose scale stays are copied; the others are one product by the ratio
+  // of the scales, in two factors where it is no fp16 number (products below
+  // 2^-10 end as zeros, however far).
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int e = (int)(__float_as_uint(s[p]) >> 23) - (int)(__float_as_uint(so) >> 23);
-    const int e1 = max(-14, min(15, e)), e2 = max(-14, min(15, e - e1));
-    const __half2 f1 = __half2half2(__ushort_as_half((uint16_t)((e1 + 15) << 10)));
-    const __half2 f2 = __half2half2(__ushort_as_half((uint16_t)((e2 + 15) << 10)));
-    const uint32_t x[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
-    uint32_t y[4];
+    if (odd || __any_sync(0xffffffffu, src[p] >= 0 && e != 0)) {
+      const int e1 = max(-14, min(15, e)), e2 = max(-14, min(15, e - e1));
+      const __half2 f1 = __half2half2(__ushort_as_half((uint16_t)((e1 + 15) << 10)));
+      const __half2 f2 = __half2half2(__ushort_as_half((uint16_t)((e2 + 15) << 10)));
+      const bool far = __any_sync(0xffffffffu, e2 != 0);
+      uint32_t x[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = e4m3x2_f16(x[j]), hi = e4m3x2_f16(x[j] >> 16);
-      const __half2 l = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&lo), f1), f2);
-      const __half2 u = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&hi), f1), f2);
-      y[j] = f16_e4m3x2(l) | (f16_e4m3x2(u) << 16);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t lo, hi;
+        e4m3x4_f16(x[j], lo, hi);
+        __half2 l = __hmul2(*reinterpret_cast<const __half2*>(&lo), f1);
+        __half2 u = __hmul2(*reinterpret_cast<const __half2*>(&hi), f1);
+        if (far) {
+          l = __hmul2(l, f2);
+          u = __hmul2(u, f2);
+        }
+        x[j] = f16_e4m3x2(l) | (f16_e4m3x2(u) << 16);
+      }
+      w[p] = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    if (src[p] >= 0)
-      *reinterpret_cast<uint4*>(to + (p * RPP + row) * go.st) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (src[p] >= 0) *reinterpret_cast<uint4*>(to + (p * RPP + row) * go.st) = w[p];
   }
   if (lane == 0 && w0 % g.blk == 0) (kv ? vso : kso)[go.scale(b, h, w0 >> lb)] = so;
 }
