@@ -1254,8 +1254,9 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
 // their new blocks: warps and tiles as in the append.  The maximum is taken
 // over fp16 pairs (codes are exact fp16 numbers, and the larger of a number
 // and a NaN is the number), one product with its scale a row.  Measured: 32768
-// tokens of 8 heads (134 MB in and out) 27 us, 4.9 TB/s, bound by the chain of
-// token number, codes, barrier and store, nine CTAs an SM deep.
+// tokens of 8 heads (134 MB in and out) 25 us, 5.4 TB/s, bound by the chain of
+// token number, codes, barrier and store, ten CTAs an SM deep (tiles of 128
+// rows for the larger blocks: 1.5 us slower).
 template <int D, int TILE>
 __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
     Kv8Geom g, Kv8Geom go, const uint8_t* __restrict__ k, const uint8_t* __restrict__ v,
