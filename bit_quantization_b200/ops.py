@@ -656,7 +656,7 @@ def _scratch(nbytes, index):
     """Workspace of a call on device ``index``: the stream's own buffer, or,
     under graph capture, memory of the graph's pool (two graphs never share
     it, and it lives as long as the graph)."""
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
     return _ws.of(nbytes, index)
 
@@ -667,15 +667,9 @@ def _own_bytes(workspace):
         raise ThriftError("workspace must be contiguous uint8")
 
 
-def _call(index, what, fn, *args):
-    """A library call with device ``index`` current (see _on)."""
-    if index == torch.cuda.current_device():
-        code = fn(*args)
-    else:
-        with torch.cuda.device(index):
-            code = fn(*args)
-    if code != OK:
-        _check(code, what)
+def _elsewhere(index):
+    """Whether device ``index`` is not the current one (see _on)."""
+    return index != torch._C._cuda_getDevice()
 
 
 def _kv8_cache(k, v, k_scale, v_scale, blk, what=""):
@@ -724,10 +718,18 @@ def thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new=Non
     if weight is not None:
         _vector(weight, B * Hkv * cap, _F32, "weight")
     index = _same_device(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new, weight, new_len)
-    _call(index, "thrift_kv8_append", lib().thrift_kv8_append, k_new.data_ptr(), v_new.data_ptr(),
-          dt, B, Hkv, d, blk, cap, sb, sh, st, cache_len.data_ptr(), _ptr(n_new), shape[1],
-          k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(weight),
-          _ptr(new_len), _raw_stream(index))
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return thrift_kv8_append(k_new, v_new, k, v, k_scale, v_scale, cache_len, n_new, blk,
+                                     weight, new_len)
+    code = lib().thrift_kv8_append(
+        k_new.data_ptr(), v_new.data_ptr(), dt, B, Hkv, d, blk, cap, sb, sh, st,
+        cache_len.data_ptr(), None if n_new is None else n_new.data_ptr(), shape[1], k.data_ptr(),
+        v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        None if weight is None else weight.data_ptr(),
+        None if new_len is None else new_len.data_ptr(), _raw_stream(index))
+    if code:
+        _check(code, "thrift_kv8_append")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -759,6 +761,10 @@ def thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk=64, scale=None, we
     if workspace is not None:
         _own_bytes(workspace)
     index = _same_device(q, k, v, k_scale, v_scale, seq_len, weight, out, lse, workspace)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk, scale, weight, out,
+                                     lse, workspace)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -766,11 +772,14 @@ def thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk=64, scale=None, we
     if workspace is None:
         workspace = _scratch(kv8_decode_workspace_size(B, H, Hkv, cap, d, weight is not None),
                              index)
-    _call(index, "thrift_kv8_decode", lib().thrift_kv8_decode, q.data_ptr(), dt, B, H, Hkv, d,
-          blk, cap, sb, sh, st, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-          seq_len.data_ptr(), d ** -0.5 if scale is None else float(scale), _ptr(weight),
-          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-          _raw_stream(index))
+    code = lib().thrift_kv8_decode(
+        q.data_ptr(), dt, B, H, Hkv, d, blk, cap, sb, sh, st, k.data_ptr(), v.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), seq_len.data_ptr(),
+        d ** -0.5 if scale is None else float(scale),
+        None if weight is None else weight.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    if code:
+        _check(code, "thrift_kv8_decode")
     return out, lse
 
 
@@ -785,9 +794,9 @@ def thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_o
     stays of each (sequence, kv head) when its tokens are cut to ``budget``:
     the first ``sink``, the last ``recent`` and the heaviest others by
     ``weight``, in their order; ``len_out`` = min(seq_len, budget)."""
-    B, Hkv, cap, d, *st = _kv8_cache(k, v, k_scale, v_scale, blk)
-    Bo, Ho, cap_o, do, *sto = _kv8_cache(k_out, v_out, k_scale_out, v_scale_out, blk, "_out")
-    if (Bo, Ho, do) != (B, Hkv, d):
+    B, Hkv, cap, d, sb, sh, st = _kv8_cache(k, v, k_scale, v_scale, blk)
+    Bo, Ho, cap_o, do, sbo, sho, sto = _kv8_cache(k_out, v_out, k_scale_out, v_scale_out, blk, "_out")
+    if Bo != B or Ho != Hkv or do != d:
         raise ThriftError("the two caches must agree in batch, heads and d")
     budget, recent, sink = int(budget), int(recent), int(sink)
     if budget < 1 or recent < 0 or sink < 0 or sink + recent > budget:
@@ -801,14 +810,21 @@ def thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_o
     _own_bytes(workspace)
     index = _same_device(k, v, k_scale, v_scale, weight, seq_len, k_out, v_out, k_scale_out,
                          v_scale_out, weight_out, len_out, workspace)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_out,
+                                    k_scale_out, v_scale_out, weight_out, len_out, blk, recent,
+                                    sink, workspace)
     if workspace is None:
         workspace = _scratch(kv8_evict_workspace_size(B, Hkv, cap, budget), index)
-    _call(index, "thrift_kv8_evict", lib().thrift_kv8_evict, B, Hkv, d, blk, cap, *st,
-          k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), weight.data_ptr(),
-          seq_len.data_ptr(), budget, sink, recent, cap_o, *sto, k_out.data_ptr(),
-          v_out.data_ptr(), k_scale_out.data_ptr(), v_scale_out.data_ptr(),
-          weight_out.data_ptr(), len_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-          _raw_stream(index))
+    code = lib().thrift_kv8_evict(
+        B, Hkv, d, blk, cap, sb, sh, st, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), weight.data_ptr(), seq_len.data_ptr(), budget, sink, recent, cap_o,
+        sbo, sho, sto, k_out.data_ptr(), v_out.data_ptr(), k_scale_out.data_ptr(),
+        v_scale_out.data_ptr(), weight_out.data_ptr(), len_out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _raw_stream(index))
+    if code:
+        _check(code, "thrift_kv8_evict")
 
 
 class KV8Cache:
@@ -875,10 +891,11 @@ def nvfp4_linear(x, codes, scales, tensor_scale, out=None, workspace=None):
     """y = x W^T: x [M, K] fp16/bf16 (M <= 64) and NVFP4 weights W [N, K] as
     nvfp4_quantize leaves them (codes u8 [N, K/2], scales u8 [N, K/16],
     tensor_scale f32 [1]) -> [M, N] in x's dtype.  K % 32 == 0."""
-    if x.dim() != 2 or codes.dim() != 2:
+    shape, wide = x.shape, codes.shape
+    if len(shape) != 2 or len(wide) != 2:
         raise ThriftError("x must be [M, K] and codes [N, K/2]")
-    M, K = x.shape
-    N, dt = codes.shape[0], _16BIT.get(x.dtype)
+    M, K = shape
+    N, dt = wide[0], _16BIT.get(x.dtype)
     if dt is None or not x.is_contiguous():
         raise ThriftError(f"x must be contiguous and of a 16-bit type, got {x.dtype}")
     if M > 64 or K == 0 or K % 32 or K > 1 << 19:
@@ -893,15 +910,20 @@ def nvfp4_linear(x, codes, scales, tensor_scale, out=None, workspace=None):
     if workspace is not None:
         _own_bytes(workspace)
     index = _same_device(x, codes, scales, tensor_scale, out, workspace)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return nvfp4_linear(x, codes, scales, tensor_scale, out, workspace)
     if out is None:
         out = x.new_empty((M, N))
     if M == 0 or N == 0:
         return out
     if workspace is None:
         workspace = _scratch(nvfp4_linear_workspace_size(M, N, K), index)
-    _call(index, "nvfp4_linear", lib().nvfp4_linear, x.data_ptr(), dt, M, N, K, codes.data_ptr(),
-          scales.data_ptr(), tensor_scale.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-          workspace.numel(), _raw_stream(index))
+    code = lib().nvfp4_linear(x.data_ptr(), dt, M, N, K, codes.data_ptr(), scales.data_ptr(),
+                              tensor_scale.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                              workspace.numel(), _raw_stream(index))
+    if code:
+        _check(code, "nvfp4_linear")
     return out
 
 
