@@ -1231,11 +1231,15 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
     eq0 += (int)__reduce_add_sync(0xffffffffu, c.y);
   }
   const unsigned below = (1u << lane) - 1u;
+  // in bounds whatever another stream may do to the weights meanwhile
+  auto put = [&](int at, bool stays, int t) {
+    if (stays && at < budget) out[at] = t;
+  };
   each([&](int t, uint32_t k) {
     const bool gt = (k & pmask) > prefix;
     const unsigned mg = __ballot_sync(0xffffffffu, gt);
     if (all) {
-      if (gt) out[gt0 + __popc(mg & below)] = t;
+      put(gt0 + __popc(mg & below), gt, t);
       gt0 += __popc(mg);
       return;
     }
@@ -1243,7 +1247,7 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
     const unsigned me = __ballot_sync(0xffffffffu, eq);
     const int e = eq0 + __popc(me & below);
     // survivors before this token: all above, and the first rem of the equal
-    if (gt || (eq && e < rem)) out[gt0 + __popc(mg & below) + min(e, rem)] = t;
+    put(gt0 + __popc(mg & below) + min(e, rem), gt || (eq && e < rem), t);
     gt0 += __popc(mg);
     eq0 += __popc(me);
   });
@@ -1282,7 +1286,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int i = w0 + p * RPP + row;
-    src[p] = i < n ? __ldcg(kept + bh * budget + i) : -1;
+    src[p] = i < n ? min(max(0, __ldcg(kept + bh * budget + i)), g.capacity - 1) : -1;
   }
   uint4 w[PASSES];
   float s[PASSES];

@@ -1606,11 +1606,13 @@ thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int
   const std::pair<const void*, int64_t> to[] = {
       {k_out, out_n}, {v_out, out_n}, {k_scale_out, sco}, {v_scale_out, sco},
       {weight_out, pairs * out_capacity * 4}, {len_out, (int64_t)B * 4}};
-  for (const auto& a : in)
-    for (const auto& b : to)
+  const size_t need = thrift_kv8_evict_workspace_size(B, Hkv, capacity, budget);
+  for (const auto& b : to) {
+    for (const auto& a : in)
       if (ranges_meet(a.first, a.second, b.first, b.second)) return THRIFT_ERR_ARG;
-  if (k_out == v_out || ws_bytes < thrift_kv8_evict_workspace_size(B, Hkv, capacity, budget))
-    return THRIFT_ERR_ARG;
+    if (ranges_meet(workspace, (int64_t)need, b.first, b.second)) return THRIFT_ERR_ARG;
+  }
+  if (k_out == v_out || ws_bytes < need) return THRIFT_ERR_ARG;
   const Kv8Geom g = kv8_geom(B, Hkv, blk, capacity, stride_b, stride_h, stride_t);
   const Kv8Geom go =
       kv8_geom(B, Hkv, blk, out_capacity, out_stride_b, out_stride_h, out_stride_t);

@@ -352,8 +352,8 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  *                   has received so far (optional but for the eviction).
  * Nothing has to be cleared: rows, scales and weights at or behind a
  * sequence's length are never read.  Supported: d in {64, 128}, blk in {16,
- * 32, 64, 128} (else THRIFT_ERR_UNSUPPORTED), H % Hkv == 0, either 16-bit
- * type.  Lengths (int32 [B] on the device) are clamped to [0, capacity].
+ * 32, 64, 128}, B <= 65535, Hkv <= 32767, capacity <= 2^30 (else
+ * THRIFT_ERR_UNSUPPORTED), H % Hkv == 0, either 16-bit type.  Lengths (int32 [B] on the device) are clamped to [0, capacity].
  *
  * Scales are powers of two: a block's is the smallest 2^e, e >= -120, with
  * max|x| <= 448 * 2^e over the finite values that entered it; a code is x /
@@ -374,7 +374,8 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  *   out 16-bit [B, H, d] out;  lse fp32 [B, H] out (natural log; an empty
  *   sequence gives a zero row and -inf);  weight (or NULL): += the sum over
  *   the query heads of each kv head of the probability of each token.
- *   A NaN among a row's inputs makes that row NaN.
+ *   A NaN or infinity among a row's inputs makes that row NaN (a value's, its
+ *   channel).  Outputs overlap no input.  B H capacity / 128 below 2^30.
  *
  * thrift_kv8_evict: writes into another cache (out_*, its own capacity >=
  * min(budget, capacity), strides, and every tensor apart from the input's)

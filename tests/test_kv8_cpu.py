@@ -163,6 +163,7 @@ def test_evict_abi_refuses(L):
         (dict(wo=P(1 << 24)), ops.ERR_ARG), (dict(lo=P(1 << 25)), ops.ERR_ARG),
         (dict(vo=P(1 << 26)), ops.ERR_ARG), (dict(w=None), ops.ERR_ARG), (dict(wb=100), ops.ERR_ARG),
         (dict(sto=32), ops.ERR_ARG), (dict(d=32), ops.ERR_UNSUPPORTED),
+        (dict(ws=P(1 << 30)), ops.ERR_ARG), (dict(st=1 << 24, sh=1 << 30, sb=1 << 31), ops.ERR_ARG),
     ):
         assert _evict(L, **kw) == want, kw
 
