@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
   constexpr int ROWS = TILE / kKv8Warps, PASSES = ROWS / RPP;
   __shared__ float red[kKv8Warps];
   const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 8 * (lane % TPR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane / TPR, c = 8 * (lane % TPR);
   pdl_wait();
   if (more) pdl_trigger();
   const int len = g.len(cache_len, b);
@@ -264,7 +265,8 @@ __global__ void __launch_bounds__(1024) kv8_append_step_kernel(
       for (int p = 0; p < PASSES; ++p) {
         const int t = first + p * RPP + row;
         uint4 raw = make_uint4(0, 0, 0, 0);
-        if (t < last) raw = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
+        if (t < last)
+          raw = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
         unpack8<DT>(raw, x[p]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[p][i]) ? fabsf(x[p][i]) : 0.0f);
@@ -374,18 +376,20 @@ struct Kv8Dec {
 // precede those of each (kv head, part): many short sequences would otherwise
 // fall to few CTAs.  A CTA has at most two stretches that others share, its
 // first and its last; one that is its own it finishes itself.
+// Lengths that another stream changes meanwhile give wrong results but no
+// access out of bounds.
 constexpr int kKv8Head = 1;
 struct Kv8Plan {
-  int total, run, longer;  // the first `longer` CTAs take run + 1 units, the others run
-  __device__ __forceinline__ void set(int units, int ctas) {
-    total = units;
-    run = units / ctas;
-    longer = units % ctas;
+  int ctas, run, longer;  // the first `longer` CTAs take run + 1 units, the others run
+  __device__ __forceinline__ void set(int units, int n) {
+    ctas = n;
+    run = units / n;
+    longer = units % n;
   }
   __device__ __forceinline__ int first(int cta) const { return run * cta + min(cta, longer); }
   __device__ __forceinline__ int owner(int unit) const {
     const int lead = longer * (run + 1);
-    return unit < lead ? unit / (run + 1) : longer + (unit - lead) / run;
+    return min(ctas - 1, unit < lead ? unit / (run + 1) : longer + (unit - lead) / max(1, run));
   }
 };
 
@@ -412,13 +416,7 @@ __device__ __forceinline__ int2 kv8_count(const Kv8Dec& p, int upto) {
                    per * __reduce_add_sync(0xffffffffu, before));
 }
 
-// Two E4M3 codes (the low or high half of c) -> two fp16 values (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return h;
-}
-// The same of both halves of c.
+// Four E4M3 codes -> four fp16 values (exact), the two low bytes first.
 __device__ __forceinline__ void e4m3x4_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
@@ -510,11 +508,12 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
       const int at = past ? __ffs(past) - 1 : 31;
       const int before = __shfl_sync(0xffffffffu, upto - mine, at);
       n = __shfl_sync(0xffffffffu, mine, at);
-      if (past || b0 + 32 >= p.g.B) {
+      if (past) {
         b = b0 + at;
         rel -= before * per;
         break;
       }
+      if (b0 + 32 >= p.g.B) return;
       rel -= (before + n) * per;
     }
     pair = rel / n;  // (kv head, part)
@@ -816,15 +815,13 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
     const bool mine = sole;
     u += jn;
     j = 0;
-    const bool more = !SOLE && uend - u > kKv8Head;
-    if (more) {
-      if (++pair == per) {
-        pair = 0;
-        do n = kv8_units<D>(p, ++b);
-        while (n == 0);
-      }
-      open();
+    bool more = !SOLE && uend - u > kKv8Head;
+    if (more && ++pair == per) {
+      pair = n = 0;
+      while (n == 0 && ++b < p.g.B) n = kv8_units<D>(p, b);
+      more = n > 0;
     }
+    if (more) open();
     // ---- ... while the CTA's warps join this one's parts
 #pragma unroll
     for (int a = 0; a < NT; ++a)
@@ -911,7 +908,8 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
       const int heads = min(p.Gc, p.G - part * p.Gc), u0 = count.y + (h * p.HG + part) * n;
       const int a = plan.owner(u0 + kKv8Head), z = plan.owner(u0 + n - 1);
       __syncthreads();  // s_norm has been read
-      for (int r = warp; r < heads; r += 8) {  // maximum and 1 / sum of a head, its CTAs over the lanes
+      // maximum and 1 / sum of a head, its CTAs over the lanes
+      for (int r = warp; r < heads; r += 8) {
         float M = -INFINITY, L = 0.0f;
         if (a == z && lane == 0) {
           const float2 ml = p.norm[(int64_t)b * p.H + h * p.G + part * p.Gc + r];
@@ -927,7 +925,8 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
-          const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+          const float m2 = __shfl_xor_sync(0xffffffffu, M, o);
+          const float l2 = __shfl_xor_sync(0xffffffffu, L, o);
           const float mn = fmaxf(M, m2), ref = mn == -INFINITY ? 0.0f : mn;
           L = L * exp2f(M - ref) + l2 * exp2f(m2 - ref);
           M = mn;
@@ -960,7 +959,8 @@ __global__ void __launch_bounds__(256, WEIGHTS ? 6 : 4) kv8_finish_kernel(const 
     return;
   }
   const int groups = (p.Gc + (1 << p.lhc) - 1) >> p.lhc, per = p.g.Hkv * p.HG;
-  const int i = blockIdx.x - (WEIGHTS ? p.weights : 0), b = i / groups / per, pair = i / groups % per;
+  const int i = blockIdx.x - (WEIGHTS ? p.weights : 0);
+  const int b = i / groups / per, pair = i / groups % per;
   const int r0 = i % groups << p.lhc;  // the first of its heads in the part
   const int heads = min(1 << p.lhc, min(p.Gc, p.G - pair % p.HG * p.Gc) - r0);
   const int64_t bh = (int64_t)b * p.H + pair / p.HG * p.G + pair % p.HG * p.Gc + r0;
@@ -1153,7 +1153,8 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
       else
         __syncthreads();
       auto theirs = [&](const uint32_t* at, int r) {
-        return r == rank ? *at : r < cl ? __float_as_uint(ld_cluster(reinterpret_cast<const float*>(at), r)) : 0u;
+        if (r == rank) return *at;
+        return r < cl ? __float_as_uint(ld_cluster(reinterpret_cast<const float*>(at), r)) : 0u;
       };
       if (tid < 64 * kKv8SelCluster) s_theirs[tid] = theirs(sums + (tid & 63), tid >> 6);
       __syncthreads();
@@ -1272,7 +1273,8 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
   constexpr int ROWS = TILE / kKv8Warps, PASSES = ROWS / RPP;
   __shared__ float red[kKv8Warps];
   const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane / TPR, c = 16 * (lane % TPR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane / TPR, c = 16 * (lane % TPR);
   const int n = min(g.len(seq_len, b), budget);
   const int w0 = (int)blockIdx.x * TILE + warp * ROWS;  // this warp's rows
   if ((int)blockIdx.x * TILE >= n) return;

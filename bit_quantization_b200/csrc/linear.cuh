@@ -96,7 +96,8 @@ __device__ __forceinline__ float2 e2m1x2_decode(uint32_t c) {
 // L2, which is quicker than asking the others), then every thread writes the
 // digits of 8 values, two threads the scale of a block of 16.
 template <int DT>
-__global__ void __launch_bounds__(kLinDigitThreads) lin_digits_kernel(const LinParams p, int parts) {
+__global__ void __launch_bounds__(kLinDigitThreads)
+    lin_digits_kernel(const LinParams p, int parts) {
   __shared__ uint32_t s_max;
   const int m = blockIdx.x / parts, rank = blockIdx.x % parts, tid = threadIdx.x;
   if (tid == 0) s_max = 0;
@@ -411,7 +412,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
       for (int m = 0; m < ROWS; ++m) {
         v[m] = 0.0f;
 #pragma unroll
-        for (int d = kLinDigits - 1; d >= 0; --d) v[m] = fmaf(v[m], 0.125f, acc[kLinDigits * m + d]);
+        for (int d = kLinDigits - 1; d >= 0; --d)
+          v[m] = fmaf(v[m], 0.125f, acc[kLinDigits * m + d]);
       }
       if (len < chunks) {
         // a shared tile: CTAs a .. b have a part of it
