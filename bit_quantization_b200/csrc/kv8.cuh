@@ -1277,13 +1277,16 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
   const int row = lane / TPR, c = 16 * (lane % TPR);
   const int n = min(g.len(seq_len, b), budget);
   const int w0 = (int)blockIdx.x * TILE + warp * ROWS;  // this warp's rows
+  // Also by a CTA without rows: where every sequence is empty nothing else
+  // would keep what follows this kernel from overtaking the select, which
+  // still writes the lengths.
+  pdl_wait();
   if ((int)blockIdx.x * TILE >= n) return;
   const int wpb = g.blk > ROWS ? g.blk / ROWS : 1;
   const int64_t bh = (int64_t)b * g.Hkv + h;
   const uint8_t* codes = (kv ? v : k) + g.row(b, h, 0) + c;
   const float* scales = (kv ? vs : ks) + g.scale(b, h, 0);
   const int lb = 31 - __clz(g.blk);  // blk is a power of two
-  pdl_wait();
   int src[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {

@@ -1,0 +1,30 @@
+"""Calls of the 8-bit cache at the ends of what they take."""
+import pytest
+import torch
+
+from bit_quantization_b200 import ops
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def _u8(t):
+    return t.cpu().view(torch.uint8)
+
+
+def test_evict_of_empty_sequences_then_an_append():
+    """Nothing to gather: the lengths that the eviction writes are what the
+    append right behind it goes by, not those the spare cache held before."""
+    gen = torch.Generator().manual_seed(1)
+    B, Hkv, cap = 64, 8, 4096
+    empty, spare = (ops.KV8Cache(B, Hkv, cap, d=64, blk=16) for _ in range(2))
+    x = torch.randn((B, 1, Hkv, 64), generator=gen).to(BF16).cuda()
+    want = ops.KV8Cache(B, Hkv, cap, d=64, blk=16)
+    want.append(x, x)
+    torch.cuda.synchronize()
+    for i in range(50):
+        spare.lengths.fill_(7 + i)  # of its previous contents
+        empty.evict(100 + i, recent=3, out=spare).append(x, x)
+        assert spare.lengths.tolist() == [1] * B
+        assert torch.equal(_u8(spare.k)[:, :, 0], _u8(want.k)[:, :, 0])
+        assert torch.equal(spare.k_scale[:, :, 0], want.k_scale[:, :, 0])
