@@ -16,9 +16,11 @@
 namespace thrift {
 
 // Every kernel here may be scheduled while the kernel before it in the stream
-// ends, and waits for it first of all.  Only one that another kernel of the
-// same call follows lets that one be scheduled early: what comes after a call
-// may read the call's results before it waits (the quantiser does).
+// ends, and waits for it before it reads or writes anything that one may have
+// written.  Only one that another kernel of the same call follows lets that
+// one be scheduled early, after its own wait: so the second may read ahead of
+// its wait what the call's first kernel does not write, and a call's results
+// are complete for whatever follows it.
 
 // ------------------------------------------------------------ conversions --
 

@@ -101,15 +101,10 @@ thrift_status thrift_stream_status(void* stream, int reset);
  *   maximum per CTA into the workspace) and a quantise kernel that reduces
  *   those maxima to g and quantises (x read twice: from L2 the second time
  *   when it fits); with the scale given, the quantise kernel alone.  Both are
- *   launched with programmatic dependent launch: a kernel's first input loads
- *   may run while the previous kernel of the stream finishes, and whatever
- *   that kernel may write (the maxima, a given tensor scale, the outputs) is
- *   touched only after it has completed.  Hence x must already be final when
- *   the previous kernel of the stream lets its dependents start: x must not
- *   alias a previous quantiser call's codes, scales or tensor scale, and a
- *   predecessor that triggers its dependents early itself
- *   (griddepcontrol.launch_dependents) must have written x before it does;
- *   every other predecessor is waited for in full.
+ *   launched with programmatic dependent launch: they may be scheduled while
+ *   the previous kernel of the stream finishes, and a call waits for that
+ *   kernel in full before it reads x or anything else, so x may be what the
+ *   call before it wrote.  x and the outputs must not overlap.
  */
 size_t nvfp4_quantize_workspace_size(void);
 thrift_status nvfp4_quantize(const void* x, thrift_dtype dt, int64_t rows, int64_t cols,

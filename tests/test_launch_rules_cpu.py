@@ -54,3 +54,18 @@ def test_the_rule_sees_an_early_return():
     assert _returns_before_the_wait("{ if (x) return; pdl_wait(); }")
     assert not _returns_before_the_wait("{ pdl_wait(); if (x) return; }")
     assert not _returns_before_the_wait("{ auto f = [&](int a) { return a; }; pdl_wait(); }")
+
+
+def test_the_quantiser_reads_x_behind_the_wait():
+    """The first kernel of a call waits for what may have written x before it
+    loads any of it, and lets the next be scheduled only after that; the second
+    may load x ahead of its own wait, the first having waited."""
+    body = dict(_kernels())
+    first = body["amax_partial_kernel"]
+    assert first.index("pdl_wait()") < first.index("load_raw(")
+    assert first.index("pdl_wait()") < first.index("pdl_trigger()")
+    rows = body["quant_rows_kernel"]
+    given = re.search(r"if \(scale_given\) pdl_wait\(\);", rows)
+    assert given and given.end() < rows.index("load_raw(")
+    cols = body["quant_cols_kernel"]
+    assert cols.index("quant_tensor_scale(") < cols.index("__ldg(x")
