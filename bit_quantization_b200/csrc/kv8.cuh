@@ -330,11 +330,17 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
 // transpose of the probabilities as S^T leaves them.  q enters as fp16, bf16
 // brought there by a power of two of the row's largest value (an element
 // 2^-28 below it and less keeps an error of 2^-39 of it).  A probability
-// enters as fp16, relative to the running maximum; sums of it are fp32.  O is
-// kept in units of the scale of the V block at hand, and moves to another
-// block's by an exact power of two.
+// enters as fp16, relative to the running maximum and times 2^15, the top of
+// fp16's range: within 2^-11 of itself down to 2^-29 of the largest, and within
+// 2^-40 of the largest below.  (Taken as it is, at most 1, all below 2^-25 of a
+// token that outweighs the others would be lost from O and not from the sum of
+// probabilities: with one 20 above 500 others and no value, an eighth of the
+// output.)  Sums of it are fp32, of the unrounded ones; O is kept in units of
+// the scale of the V block at hand, and moves to another block's by an exact
+// power of two, as it comes back from the factor 2^15.
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kKv8ProbUp = 32768.0f;  // of a probability's fp16 form
 constexpr int kKv8DecWarps = 4;
 __host__ __device__ constexpr int kv8_dec_ctas(int nt) { return nt > 1 ? 2 : 3; }  // an SM
 constexpr int kKv8MaxCtas = 512;
@@ -787,11 +793,9 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
             pr[e] = ex2(sv[i][a][e] - ref[a][e & 1]);
             l[a][e & 1] += pr[e];
           }
-          if (vsc[i] != unit) {
-            const float ratio = vsc[i] / unit;
+          const float up = vsc[i] == unit ? kKv8ProbUp : kKv8ProbUp * (vsc[i] / unit);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pr[e] *= ratio;
-          }
+          for (int e = 0; e < 4; ++e) pr[e] *= up;
           b0[a] = transpose_8x8(pack_f16(pr[0], pr[1]));
           b1[a] = transpose_8x8(pack_f16(pr[2], pr[3]));
         }
@@ -825,6 +829,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
     }
     if (more) open();
     // ---- ... while the CTA's warps join this one's parts
+    const float down = unit * (1.0f / kKv8ProbUp);
 #pragma unroll
     for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -841,7 +846,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            s_o[warp][8 * a + 2 * t + e][(D / 8) * gr + 2 * s + r] = o[a][s][2 * r + e] * unit;
+            s_o[warp][8 * a + 2 * t + e][(D / 8) * gr + 2 * s + r] = o[a][s][2 * r + e] * down;
       }
     __syncthreads();
     const int64_t slot = 2 * (int64_t)blockIdx.x + (seg > 0);

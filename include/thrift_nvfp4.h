@@ -371,6 +371,8 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  *   the query heads of each kv head of the probability of each token.
  *   A NaN or infinity among a row's inputs makes that row NaN (a value's, its
  *   channel).  Outputs overlap no input.  B H capacity / 128 below 2^30.
+ *   Scores, the softmax and all sums are fp32; a probability multiplies v
+ *   within 2^-11 of itself, or 2^-40 of its row's largest.
  *
  * thrift_kv8_evict: writes into another cache (out_*, its own capacity >=
  * min(budget, capacity), strides, and every tensor apart from the input's)
