@@ -10,6 +10,8 @@
 // below E4M3's normal range there.  A growing block can therefore be
 // rescaled, and an evicted cache re-blocked, without a 16-bit copy.
 #pragma once
+#include <cfloat>
+
 #include "select.cuh"
 #include "tc.cuh"
 
@@ -1334,7 +1336,8 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
     }
     const float2 f = __half22float2(top);
     const float y = fmaxf(f.x, f.y) * fabsf(s[p]);
-    a = fmaxf(a, finite_f(y) ? y : 0.0f);
+    // 256 * 2^120, what the largest bf16 values round to, is no fp32 number
+    a = fmaxf(a, finite_f(y) ? y : finite_f(s[p]) ? FLT_MAX : 0.0f);
   }
   const bool odd = __any_sync(0xffffffffu, nan != 0);
   a = warp_max(a);

@@ -28,3 +28,23 @@ def test_evict_of_empty_sequences_then_an_append():
         assert spare.lengths.tolist() == [1] * B
         assert torch.equal(_u8(spare.k)[:, :, 0], _u8(want.k)[:, :, 0])
         assert torch.equal(spare.k_scale[:, :, 0], want.k_scale[:, :, 0])
+
+
+@pytest.mark.parametrize("blk", [16, 128])
+def test_evict_keeps_codes_that_stand_for_two_to_the_128(blk):
+    """The largest bf16 values round to a code 256 * 2^120: a number, although
+    not one of fp32.  It counts for the new block's scale as it did for the
+    old one's."""
+    n = 2 * blk
+    x = torch.ones((1, n, 1, 64), dtype=BF16, device="cuda")
+    x[0, 3, 0, 5] = torch.finfo(BF16).max
+    x[0, blk, 0, 7] = -torch.finfo(BF16).max
+    c = ops.KV8Cache(1, 1, n, d=64, blk=blk)
+    c.append(x, x)
+    assert c.k_scale.tolist() == [[[2.0 ** 120] * 2]]
+    c.weight.copy_(torch.arange(n, 0, -1.0))  # the first ones stay
+    cut = c.evict(n - 1)
+    assert cut.lengths.tolist() == [n - 1]
+    assert cut.k_scale.tolist() == [[[2.0 ** 120] * 2]]
+    assert torch.equal(_u8(cut.k)[0, 0, :n - 1], _u8(c.k)[0, 0, :n - 1])
+    assert torch.equal(_u8(cut.v)[0, 0, :n - 1], _u8(c.v)[0, 0, :n - 1])
