@@ -803,6 +803,8 @@ def thrift_kv8_evict(k, v, k_scale, v_scale, weight, seq_len, budget, k_out, v_o
         raise ThriftError("budget must be positive and at least sink + recent")
     if cap_o < min(budget, cap):
         raise ThriftError(f"the cache written to holds {cap_o} tokens, the budget is {budget}")
+    if budget >= cap:  # everything stays: of any size, past the library's 32 bits too
+        budget, recent, sink = cap, 0, 0
     _vector(weight, B * Hkv * cap, torch.float32, "weight")
     _vector(weight_out, B * Hkv * cap_o, torch.float32, "weight_out")
     _vector(seq_len, B, torch.int32, "seq_len")

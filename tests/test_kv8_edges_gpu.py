@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import kv8_ref as ref
 from bit_quantization_b200 import ops
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,21 @@ def test_evict_keeps_codes_that_stand_for_two_to_the_128(blk):
     assert cut.k_scale.tolist() == [[[2.0 ** 120] * 2]]
     assert torch.equal(_u8(cut.k)[0, 0, :n - 1], _u8(c.k)[0, 0, :n - 1])
     assert torch.equal(_u8(cut.v)[0, 0, :n - 1], _u8(c.v)[0, 0, :n - 1])
+
+
+@pytest.mark.parametrize("budget,recent,sink", [
+    ((1 << 32) + 5, 0, 0), (1 << 40, (1 << 33) + 7, 1 << 34), (40, 20, 20), (1 << 31, 3, 4),
+])
+def test_a_budget_beyond_the_cache_keeps_everything(budget, recent, sink):
+    gen = torch.Generator().manual_seed(1)
+    c = ops.KV8Cache(2, 1, 40, d=64, blk=16)
+    x = torch.randn((2, 40, 1, 64), generator=gen).to(BF16).cuda()
+    c.append(x, -x, torch.tensor([40, 13], dtype=torch.int32, device="cuda"))
+    cut = c.evict(budget, recent=recent, sink=sink)
+    assert cut.lengths.tolist() == [40, 13]
+    for b, n in ((0, 40), (1, 13)):
+        for i in (0, 1):  # encoded anew: a largest value that was rounded may need a smaller scale
+            codes, scales = ref.reblock(_u8(c.tensors[i])[b, 0], c.tensors[2 + i][b, 0].cpu(),
+                                        list(range(n)), 16)
+            assert torch.equal(_u8(cut.tensors[i])[b, 0, :n], codes)
+            assert torch.equal(cut.tensors[2 + i][b, 0, :len(scales)].cpu(), scales)
