@@ -1536,7 +1536,8 @@ thrift_status thrift_kv8_decode(const void* q, thrift_dtype dt, int B, int H, in
   thrift_status s = kv8_shape(B, Hkv, d, blk, capacity);
   if (s != THRIFT_OK) return s;
   if (dt != THRIFT_F16 && dt != THRIFT_BF16) return THRIFT_ERR_ARG;
-  if (H <= 0 || H % Hkv || !(std::fabs(scale) <= 3.0e38f)) return THRIFT_ERR_ARG;
+  // scores are kept in log2 units
+  if (H <= 0 || H % Hkv || !std::isfinite(scale * kLog2e)) return THRIFT_ERR_ARG;
   if (!q || !k || !v || !k_scale || !v_scale || !seq_len || !out || !lse || !workspace)
     return THRIFT_ERR_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))

@@ -365,7 +365,8 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  * may be cache_len itself, else must not overlap it.
  *
  * thrift_kv8_decode: q 16-bit [B, H, d]; per (sequence, head) the softmax of
- * scale * (q . k_t) over the seq_len[b] cached tokens, applied to v.
+ * scale * (q . k_t) over the seq_len[b] cached tokens, applied to v.  |scale|
+ * log2(e) has to be a finite fp32 number.
  *   out 16-bit [B, H, d] out;  lse fp32 [B, H] out (natural log; an empty
  *   sequence gives a zero row and -inf);  weight (or NULL): += the sum over
  *   the query heads of each kv head of the probability of each token.
