@@ -263,8 +263,8 @@ class Workspace:
         self.bufs = {}
 
     def get(self, nbytes: int, device) -> torch.Tensor:
-        device = torch.device(device)
-        return self.of(nbytes, device.index)
+        index = torch.device(device).index
+        return self.of(nbytes, torch.cuda.current_device() if index is None else index)
 
     def of(self, nbytes: int, index: int) -> torch.Tensor:
         key = (index, _raw_stream(index))
