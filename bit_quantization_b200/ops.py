@@ -195,7 +195,10 @@ def _need_cuda(*ts):
 
 
 def _raw_stream(index: int) -> int:
-    """The current stream's handle on device ``index``."""
+    """The current stream's handle on device ``index``: what
+    ``torch.cuda.current_stream(index).cuda_stream`` is, by a name of torch's
+    own generated code (0.07 us against 1.3, asked for twice in a call of 10).
+    The only private name of torch here."""
     return torch._C._cuda_getCurrentRawStream(index)
 
 
@@ -656,7 +659,7 @@ def _scratch(nbytes, index):
     """Workspace of a call on device ``index``: the stream's own buffer, or,
     under graph capture, memory of the graph's pool (two graphs never share
     it, and it lives as long as the graph)."""
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
     return _ws.of(nbytes, index)
 
@@ -669,7 +672,7 @@ def _own_bytes(workspace):
 
 def _elsewhere(index):
     """Whether device ``index`` is not the current one (see _on)."""
-    return index != torch._C._cuda_getDevice()
+    return index != torch.cuda.current_device()
 
 
 def _kv8_cache(k, v, k_scale, v_scale, blk, what=""):
