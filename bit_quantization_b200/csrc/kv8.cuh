@@ -346,11 +346,18 @@ constexpr float kKv8ProbUp = 32768.0f;  // of a probability's fp16 form
 constexpr int kKv8DecWarps = 4;
 __host__ __device__ constexpr int kv8_dec_ctas(int nt) { return nt > 1 ? 2 : 3; }  // an SM
 constexpr int kKv8MaxCtas = 512;
-// Up to this capacity, and while every (sequence, kv head) has an SM, a CTA of
-// 8 warps takes all of one (up to 8 heads): 500 of 1024 tokens take 8.4 us
-// against 8.9 for the split and its merge and a full cache 11.8 against 9.2,
-// but a call costs the host a launch (2.4 us) less.
-constexpr int kKv8SoleTokens = 1024, kKv8SoleWarps = 8;
+// While every (sequence, kv head) has an SM and its capacity is at most four
+// steps of a CTA of 8 warps (1024 tokens, d = 64: 2048), such a CTA takes all
+// of one (up to 8 heads).  The length is not known on the host, so that the
+// rule weighs a whole run of a cache, from empty to full.  8 pairs, d = 128,
+// G = 4, in a graph: 3.8, 6.5, 8.2, 9.3 us for 64, 512, 768, 1024 tokens against
+// 5.7, 6.9, 6.9, 6.9 for the split and its merge (d = 64, G = 8: 3.7, 6.4, 9.9
+// for 128, 1024, 2048 against 6.2, 7.2, 7.2); a call from the host, which has a
+// launch less, 15.1 against 17.6 at every length.  So either form is at most 3
+// us behind the other up to there; at twice that capacity a full cache is 7 us
+// behind (14.2 against 7.9 at 2048).  With more pairs than SMs the second round
+// of CTAs costs more: 64 sequences of 8 heads and 1024 tokens 40.6 against 34.0.
+constexpr int kKv8SoleWarps = 8, kKv8SoleSteps = 4;
 constexpr int kKv8HeadGroup = 16;                 // query heads in one pass over the cache
 
 // Tokens a warp takes at a time, and a CTA.

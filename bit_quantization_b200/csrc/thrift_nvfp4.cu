@@ -752,7 +752,8 @@ size_t kv8_decode_plan(int B, int H, int Hkv, int capacity, int d, bool weights,
 template <int DT, int D>
 thrift_status kv8_decode_impl(Kv8Dec p, cudaStream_t st) {
   const int nt = p.Gc > 8 ? 2 : 1, pairs = p.g.B * p.g.Hkv * p.HG;
-  if (nt == 1 && !p.weight && p.g.capacity <= kKv8SoleTokens && pairs <= sm_count()) {
+  if (nt == 1 && !p.weight && pairs <= sm_count() &&
+      p.g.capacity <= kKv8SoleSteps * kKv8SoleWarps * kv8_step(D)) {
     const cudaError_t e = launch_pdl(kv8_decode_kernel<DT, D, 1, kKv8SoleWarps, true>, dim3(pairs),
                                      32 * kKv8SoleWarps, st, p);
     return e != cudaSuccess ? THRIFT_ERR_CUDA : launch_status();

@@ -110,3 +110,20 @@ def test_flat_rows_are_exact(n, G, d, dtype):
         assert torch.equal(out, want)
         assert ((lse.double() - math.log(n)).abs() <= 2.0 ** -22 * (math.log(n) + 1)).all()
     assert ((c.weight.double() * n / G - 1).abs() <= (2 * G + 4) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("cap,B,Hkv,G,d", [
+    (1024, 1, 8, 4, 128), (1025, 1, 8, 4, 128), (2048, 2, 2, 8, 64), (2049, 2, 2, 8, 64),
+    (1024, 18, 8, 2, 128), (1024, 19, 8, 2, 128), (2048, 1, 1, 9, 64),
+])
+def test_one_launch_or_two(cap, B, Hkv, G, d):
+    """Both sides of the rule that has a short cache attended to in one launch,
+    full and at the edges of its steps."""
+    gen = torch.Generator(device="cuda").manual_seed(cap + B)
+    kn, vn = (torch.randn((B, cap, Hkv, d), generator=gen, device="cuda") for _ in range(2))
+    c = _fill(kn.to(BF16), (vn + 2).to(BF16), 16, cap)
+    q = torch.randn((B, Hkv * G, d), generator=gen, device="cuda").to(BF16)
+    for n in (1, 255, 256, 513, 1023, cap):
+        c.lengths.fill_(n)
+        out, lse = c.decode(q)
+        _check(c, q, n, out, lse, d ** -0.5)
