@@ -746,7 +746,9 @@ def thrift_kv8_decode(q, k, v, k_scale, v_scale, seq_len, blk=64, scale=None, we
     [B], device) cached tokens of an 8-bit cache (see thrift_kv8_append);
     ``scale`` defaults to 1/sqrt(d).  ``weight`` (f32 [B, Hkv, capacity])
     accumulates each token's probability, summed over the query heads of its
-    kv head."""
+    kv head; scratch then holds every score, about 4 B H capacity bytes, which
+    the binding keeps per stream unless ``workspace`` is given
+    (kv8_decode_workspace_size bytes)."""
     B, Hkv, cap, d, sb, sh, st = _kv8_cache(k, v, k_scale, v_scale, blk)
     shape = q.shape
     if len(shape) != 3 or shape[0] != B or shape[2] != d or shape[1] % Hkv:

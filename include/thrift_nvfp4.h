@@ -374,6 +374,8 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  *   channel).  Outputs overlap no input.  B H capacity / 128 below 2^30.
  *   Scores, the softmax and all sums are fp32; a probability multiplies v
  *   within 2^-11 of itself, or 2^-40 of its row's largest.
+ *   Sums come before the division: the sum over the tokens of |v| times the
+ *   probability over the row's largest one has to stay an fp32 number.
  *
  * thrift_kv8_evict: writes into another cache (out_*, its own capacity >=
  * min(budget, capacity), strides, and every tensor apart from the input's)
@@ -386,7 +388,11 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  * it and their blocks keep what they held.  sink + recent <= budget.
  *
  * Workspaces: *_workspace_size bytes, 16-byte aligned, no initial content;
- * calls that overlap on the GPU must not share one. */
+ * calls that overlap on the GPU must not share one.  A decode with weights
+ * keeps every score until the row's sum is known: about 4 B H capacity bytes
+ * (each kv head's heads rounded up to even parts of at most 16), by the
+ * capacity and not the lengths: 2.1 GB for 64 sequences of 64 heads with room
+ * for 131072 tokens; at most 8.6 MB without weights. */
 thrift_status thrift_kv8_append(const void* k_new, const void* v_new, thrift_dtype dt, int B,
                                 int Hkv, int d, int blk, int capacity, int64_t stride_b,
                                 int64_t stride_h, int64_t stride_t, const int32_t* cache_len,
