@@ -67,3 +67,43 @@ def test_a_budget_beyond_the_cache_keeps_everything(budget, recent, sink):
                                         list(range(n)), 16)
             assert torch.equal(_u8(cut.tensors[i])[b, 0, :n], codes)
             assert torch.equal(cut.tensors[2 + i][b, 0, :len(scales)].cpu(), scales)
+
+
+def test_captured_prompt_append_and_eviction_replay():
+    """A prompt's append (two launches) and the eviction (a cluster launch and
+    the gather), captured on one stream and replayed between eager calls that
+    change lengths, weights and tokens."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    B, Hkv, d, blk, cap, T = 3, 2, 64, 32, 20000, 9000
+    c, spare, want = (ops.KV8Cache(B, Hkv, cap, d=d, blk=blk) for _ in range(3))
+    x = torch.randn((B, T, Hkv, d), generator=gen, device="cuda").to(BF16)
+    n = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    c.append(x, -x, n)  # warm
+    c.evict(5000, recent=100, sink=4, out=spare)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        c.append(x, -x, n)
+        c.evict(5000, recent=100, sink=4, out=spare)
+    for lengths, counts in (([0, 0, 0], [T, 1, 0]), ([7000, 20000, 31], [T, 5, 4970]),
+                            ([0, 0, 0], [0, 0, 0]), ([19999, 12000, 5000], [1, T, 0])):
+        x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+        n.copy_(torch.tensor(counts, dtype=torch.int32))
+        c.lengths.copy_(torch.tensor(lengths, dtype=torch.int32))
+        c.weight.copy_(torch.rand(c.weight.shape, generator=gen, device="cuda"))
+        spare.lengths.fill_(77)
+        before = [t.clone() for t in (*c.tensors, c.weight, c.lengths)]
+        graph.replay()
+        got = [t.clone() for t in (*spare.tensors, spare.weight, spare.lengths)]
+        for t, old in zip((*c.tensors, c.weight, c.lengths), before):
+            t.copy_(old)
+        c.append(x, -x, n)
+        c.evict(5000, recent=100, sink=4, out=want)
+        torch.cuda.synchronize()
+        kept = [min(5000, cap, a + b) for a, b in zip(lengths, counts)]
+        assert got[5].tolist() == kept == want.lengths.tolist()
+        for b, m in enumerate(kept):
+            for g, w in zip(got[:2], want.tensors[:2]):
+                assert torch.equal(_u8(g)[b, :, :m], _u8(w)[b, :, :m])
+            for g, w in zip(got[2:4], want.tensors[2:]):
+                assert torch.equal(g[b, :, :-(-m // blk)], w[b, :, :-(-m // blk)])
+            assert torch.equal(got[4][b, :, :m], want.weight[b, :, :m])
