@@ -319,9 +319,11 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
 // to registers, 32 (d = 64: 64) at a time, the next ones' keys while the
 // values of these are used and the other way round; nothing is staged, no warp
 // waits for another before its tokens are done.  Measured: 4 sequences of
-// 131072 tokens, 8 kv heads of 128, G = 4: 171 us, 6.3 TB/s; 32 of 4000 to 8192
-// with weights 86 us; G = 16 runs at 3.6 TB/s, bound by the latency of 8 warps
-// an SM.
+// 131072 tokens, 8 kv heads of 128, G = 4: 172 us, 6.2 TB/s, and 180 once the
+// card is at its power limit (a tenth of a second on); 32 of 4000 to 8192 with
+// weights 86 us; G = 16 244 us, 4.4 TB/s, bound by the latency of 8 warps an
+// SM; more heads read the cache once per 16 of them (32 heads over one kv head,
+// 16 x 32768 tokens: 71 us, a reading is 20).
 //
 //   S^T [16 tokens, 8 heads] = K Q^T, O^T [16 channels, 8 heads] += V^T P^T
 //
@@ -337,7 +339,9 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
 // 2^-40 of the largest below.  (Taken as it is, at most 1, all below 2^-25 of a
 // token that outweighs the others would be lost from O and not from the sum of
 // probabilities: with one 20 above 500 others and no value, an eighth of the
-// output.)  Sums of it are fp32, of the unrounded ones; O is kept in units of
+// output.  A second product with what the rounding leaves takes fp16 outputs
+// from 2.8e-4 of their norm to the 2.1e-4 of an fp32 form, and 8 to 10% more
+// time: not kept.)  Sums of it are fp32, of the unrounded ones; O is kept in units of
 // the scale of the V block at hand, and moves to another block's by an exact
 // power of two, as it comes back from the factor 2^15.
 

@@ -370,6 +370,8 @@ thrift_status thrift_attn_decode(const void* q, thrift_dtype dt, int B, int H, i
  *   out 16-bit [B, H, d] out;  lse fp32 [B, H] out (natural log; an empty
  *   sequence gives a zero row and -inf);  weight (or NULL): += the sum over
  *   the query heads of each kv head of the probability of each token.
+ *   The cache is read once for up to 16 query heads a kv head, ceil(H / Hkv /
+ *   16) times for more.
  *   A NaN or infinity among a row's inputs makes that row NaN (a value's, its
  *   channel).  Outputs overlap no input.  B H capacity / 128 below 2^30.
  *   Scores, the softmax and all sums are fp32; a probability multiplies v
@@ -424,6 +426,8 @@ thrift_status thrift_kv8_evict(int B, int Hkv, int d, int blk, int capacity, int
  * out 16-bit [M, N] in x's type.  nvfp4_quantize takes at most 4096 columns;
  * wider weights are quantised as [N * K / c, c] for a c that divides K (the
  * same bytes).  A row of x holding a value that is not finite gives NaN.
+ * A value of x is held within 2^-16 of the largest of its 16-block and 2^-33
+ * of its row's; sums are fp32.  The weights are read once per 16 rows.
  * Requirements: 0 <= M <= 64, K % 32 == 0 and K <= 524288 (else
  * THRIFT_ERR_UNSUPPORTED), all pointers 16-byte aligned, contiguous; out
  * overlaps no input.  Workspace: nvfp4_linear_workspace_size bytes, no initial
