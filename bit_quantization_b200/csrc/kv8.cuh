@@ -120,7 +120,7 @@ struct Kv8Geom {
     return ((int64_t)b * Hkv + h) * nblk + j;
   }
   __device__ __forceinline__ int len(const int32_t* lens, int b) const {
-    return min(capacity, max(0, __ldg(lens + b)));
+    return min(capacity, max(0, ld_behind(lens + b)));
   }
 };
 
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
   pdl_wait();
   if (more) pdl_trigger();
   const int len = g.len(cache_len, b);
-  const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
+  const int n = n_new ? min(max_new, max(0, ld_behind(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
   const int64_t tile0 = (int64_t)(len / g.blk) * g.blk + (int64_t)blockIdx.x * TILE;
   if (tile0 >= end || end == len) return;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(
     const int t = w0 + p * RPP + row;
     raw[p] = make_uint4(0, 0, 0, 0);
     if (t >= len && t < end)
-      raw[p] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
+      raw[p] = ld_behind(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
   }
   uint32_t bits = 0;
 #pragma unroll
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(1024) kv8_append_step_kernel(
   const int row = lane / TPR, c = 8 * (lane % TPR);
   pdl_wait();
   const int len = min(g.capacity, max(0, cache_len[b]));
-  const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
+  const int n = n_new ? min(max_new, max(0, ld_behind(n_new + b))) : max_new;
   const int end = (int)min((int64_t)g.capacity, (int64_t)len + n);
   for (int u = warp; u < 2 * g.Hkv; u += blockDim.x >> 5) {
     const int h = u >> 1, kv = u & 1;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(1024) kv8_append_step_kernel(
         const int t = first + p * RPP + row;
         uint4 raw = make_uint4(0, 0, 0, 0);
         if (t < last)
-          raw = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
+          raw = ld_behind(reinterpret_cast<const uint4*>(src + (int64_t)(t - len) * g.Hkv * D));
         unpack8<DT>(raw, x[p]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_f(x[p][i]) ? fabsf(x[p][i]) : 0.0f);
@@ -304,7 +304,7 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   pdl_wait();  // the append still reads cache_len
   if (b >= g.B) return;
-  const int n = n_new ? min(max_new, max(0, __ldg(n_new + b))) : max_new;
+  const int n = n_new ? min(max_new, max(0, ld_behind(n_new + b))) : max_new;
   const int len = min(g.capacity, max(0, cache_len[b]));
   new_len[b] = (int)min((int64_t)g.capacity, (int64_t)len + n);
 }
@@ -457,14 +457,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ uint4 ldg_stream16(const uint8_t* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
 }
 __device__ __forceinline__ uint2 ldg_stream8(const uint8_t* p) {
   uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
                : "=r"(r.x), "=r"(r.y)
                : "l"(p));
   return r;
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i)
-      ksc[i] = first + 16 * i < len ? __ldg(ksp + ((first + 16 * i) >> lb)) : 1.0f;
+      ksc[i] = first + 16 * i < len ? ld_behind(ksp + ((first + 16 * i) >> lb)) : 1.0f;
   };
   auto load_v = [&](int first) {
     const uint8_t* base = vb + (int64_t)first * p.g.st;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i)
-      vsc[i] = first + 16 * i < len ? __ldg(vsp + ((first + 16 * i) >> lb)) : 0.0f;
+      vsc[i] = first + 16 * i < len ? ld_behind(vsp + ((first + 16 * i) >> lb)) : 0.0f;
   };
   auto open = [&] {
     const int h = pair / p.HG, part = pair - h * p.HG;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
       const int r = warp + W * i;
 #pragma unroll
       for (int x = 0; x < D / 64; ++x)
-        qraw[i][x] = r < heads ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D) + x) : 0u;
+        qraw[i][x] = r < heads ? ld_behind(reinterpret_cast<const uint32_t*>(q + r * D) + x) : 0u;
     }
     kb = p.k + p.g.row(b, h, 0);
     vb = p.v + p.g.row(b, h, 0);
@@ -1119,7 +1119,7 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
   if constexpr (KEEP > 0) {
     float x[KEEP];  // every load is on its way before the first is waited for
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) x[i] = __ldg(w + min(from + 32 * i + lane, len - 1));
+    for (int i = 0; i < KEEP; ++i) x[i] = ld_behind(w + min(from + 32 * i + lane, len - 1));
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) key[i] = key_of(from + 32 * i + lane, x[i]);
   }
@@ -1133,7 +1133,7 @@ __global__ void __launch_bounds__(kKv8SelThreads) kv8_select_kernel(
       for (int i = 0; i < steps; i += 8) {
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __ldg(w + min(from + 32 * (i + j) + lane, len - 1));
+        for (int j = 0; j < 8; ++j) x[j] = ld_behind(w + min(from + 32 * (i + j) + lane, len - 1));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int t = from + 32 * (i + j) + lane;
@@ -1311,7 +1311,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int i = w0 + p * RPP + row;
-    src[p] = i < n ? min(max(0, __ldcg(kept + bh * budget + i)), g.capacity - 1) : -1;
+    src[p] = i < n ? min(max(0, ld_behind_l2(kept + bh * budget + i)), g.capacity - 1) : -1;
   }
   uint4 w[PASSES];
   float s[PASSES];

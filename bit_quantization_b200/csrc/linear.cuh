@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kLinDigitThreads)
   uint32_t a = 0;  // bits of |x|: ordered, infinities and NaN on top
 #pragma unroll 4
   for (int i = tid; i < n8; i += kLinDigitThreads) {
-    const uint4 v = __ldg(src + i);
+    const uint4 v = ld_behind(src + i);
     const uint32_t w = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
     a = __vmaxu2(a, w);
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kLinDigitThreads)
   // the last chunk is written to its end: its weights are zeros there, x too
   for (int i = first; i < p.chunks * (kLinChunk / 8); i += step) {
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (i < n8 && finite) v = __ldg(src + i);
+    if (i < n8 && finite) v = ld_behind(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float x[8], top8 = 0.0f;
 #pragma unroll
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
         const float* theirs = part + (int64_t)2 * a * ROWS * 128;
 #pragma unroll
         for (int m = 0; m < ROWS; ++m)
-          v[m] = m < M ? __ldcg(theirs + (second * ROWS + m) * 128) : 0.0f;
+          v[m] = m < M ? ld_behind_l2(theirs + (second * ROWS + m) * 128) : 0.0f;
         for (int i = 1; i <= b - a; i += BATCH) {
           float got[BATCH][ROWS];
 #pragma unroll
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(
 #pragma unroll
             for (int m = 0; m < ROWS; ++m)
               got[j][m] = i + j <= b - a && m < M
-                              ? __ldcg(theirs + (int64_t)(2 * (i + j) * ROWS + m) * 128)
+                              ? ld_behind_l2(theirs + (int64_t)(2 * (i + j) * ROWS + m) * 128)
                               : 0.0f;
 #pragma unroll
           for (int j = 0; j < BATCH; ++j)

@@ -131,6 +131,46 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads of what an earlier kernel of the stream may have written while this
+// one was already scheduled, behind pdl_wait.  A read-only load (__ldg, or one
+// through const __restrict__) says that nothing writes the memory while the
+// kernel exists, and may be moved ahead of the wait; these stay behind it.
+// _l2: past the first-level cache, for words that are read once.
+__device__ __forceinline__ uint32_t ld_behind(const uint32_t* p) {
+  uint32_t r;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ int32_t ld_behind(const int32_t* p) {
+  return (int32_t)ld_behind(reinterpret_cast<const uint32_t*>(p));
+}
+__device__ __forceinline__ float ld_behind(const float* p) {
+  return __uint_as_float(ld_behind(reinterpret_cast<const uint32_t*>(p)));
+}
+__device__ __forceinline__ uint4 ld_behind(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_behind_l2(const uint32_t* p) {
+  uint32_t r;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ int32_t ld_behind_l2(const int32_t* p) {
+  return (int32_t)ld_behind_l2(reinterpret_cast<const uint32_t*>(p));
+}
+__device__ __forceinline__ float ld_behind_l2(const float* p) {
+  return __uint_as_float(ld_behind_l2(reinterpret_cast<const uint32_t*>(p)));
+}
+__device__ __forceinline__ uint16_t ld_behind_l2(const uint16_t* p) {
+  uint16_t r;
+  asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
+}
+
 // ------------------------------------------------- bulk copies (TMA unit) --
 
 // Contiguous global -> shared copy completing on `bar` (transaction bytes).

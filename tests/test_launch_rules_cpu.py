@@ -57,15 +57,46 @@ def test_the_rule_sees_an_early_return():
 
 
 def test_the_quantiser_reads_x_behind_the_wait():
-    """The first kernel of a call waits for what may have written x before it
-    loads any of it, and lets the next be scheduled only after that; the second
-    may load x ahead of its own wait, the first having waited."""
+    """Every kernel of a call waits for what may have written x before it loads
+    any of it, and the first lets the next be scheduled only after that."""
     body = dict(_kernels())
-    first = body["amax_partial_kernel"]
-    assert first.index("pdl_wait()") < first.index("load_raw(")
-    assert first.index("pdl_wait()") < first.index("pdl_trigger()")
-    rows = body["quant_rows_kernel"]
-    given = re.search(r"if \(scale_given\) pdl_wait\(\);", rows)
-    assert given and given.end() < rows.index("load_raw(")
+    for name in ("amax_partial_kernel", "quant_rows_kernel"):
+        wait = re.search(r"\n  pdl_wait\(\);", body[name])  # of every thread, on every path
+        assert wait and wait.start() < body[name].index("load_raw("), name
+        assert wait.start() < body[name].index("pdl_trigger()"), name
     cols = body["quant_cols_kernel"]
-    assert cols.index("quant_tensor_scale(") < cols.index("__ldg(x")
+    assert cols.index("quant_tensor_scale(") < cols.index("ld_behind_l2(x")
+
+
+# Read-only loads of the call's inputs alone (weights' scales, the tensor scale;
+# the cache's scales and weights), which are final before the call's first
+# kernel, having waited, lets these start.
+READ_ONLY_LOADS = {"linear_kernel", "kv8_gather_kernel"}
+
+
+def test_what_the_kernel_before_may_have_written_is_not_loaded_as_read_only():
+    """A read-only load says that nothing writes the memory while the kernel
+    exists: of a kernel that is scheduled early that is not so, and the load
+    may be moved ahead of the wait."""
+    for name, body in _kernels():
+        if "pdl_wait()" in body or "quant_tensor_scale(" in body:
+            assert bool(re.search(r"__ldg\(", body)) == (name in READ_ONLY_LOADS), name
+            assert "__ldcg(" not in body, name
+    for name in ("kv8.cuh", "linear.cuh", "tc.cuh"):
+        with open(os.path.join(CSRC, name)) as f:
+            assert "ld.global.nc" not in f.read(), name
+    with open(os.path.join(CSRC, "quant_kernels.cuh")) as f:
+        raw = re.search(r"void load_raw\(.*?\n\}", f.read(), re.S).group(0)
+    assert raw.count("ld_behind(") == 2 and "__ldg" not in raw
+    with open(os.path.join(CSRC, "kv8.cuh")) as f:
+        geom = re.search(r"struct Kv8Geom \{.*?\n\};", f.read(), re.S).group(0)
+    assert "ld_behind(lens + b)" in geom and "__ldg" not in geom
+
+
+def test_loads_behind_a_wait_stay_there():
+    """Each is volatile, as the wait is: neither passes the other."""
+    with open(os.path.join(CSRC, "tc.cuh")) as f:
+        text = f.read()
+    loads = re.findall(r"asm(?: volatile)?\(\"ld\.global[^\"]*", text)
+    assert len(loads) >= 4 and all(x.startswith("asm volatile") for x in loads)
+    assert 'asm volatile("griddepcontrol.wait;" ::: "memory")' in text

@@ -33,3 +33,31 @@ def test_codes_of_the_previous_call_as_input(rows, cols, had, given):
         torch.cuda.synchronize()
         for a, b in zip(want, y):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("colblocks", [False, True])
+@pytest.mark.parametrize("rows", [512, 65536])
+def test_many_calls_in_a_row(rows, colblocks):
+    """Two hundred pairs without a stop, the second call of each with the scale
+    given, on what the first has just written over the last pair's."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    codes = torch.empty((rows, 128), dtype=torch.uint8, device="cuda")
+    xs = [torch.rand((rows, 256), generator=gen, device="cuda").half() for _ in range(3)]
+    g = torch.tensor([0.7], device="cuda")
+
+    def second():
+        y = codes.view(torch.float16)
+        return (ops.nvfp4_quantize_colblocks if colblocks else ops.nvfp4_quantize)(
+            y, tensor_scale=g)[0]
+
+    want = []
+    for x in xs:
+        ops.nvfp4_quantize(x, codes=codes)
+        torch.cuda.synchronize()
+        want.append(second())
+        torch.cuda.synchronize()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(200):
+        ops.nvfp4_quantize(xs[i % 3], codes=codes)
+        wrong += (second() != want[i % 3]).sum()
+    assert int(wrong) == 0
