@@ -319,8 +319,8 @@ __global__ void kv8_advance_kernel(Kv8Geom g, int max_new, const int32_t* cache_
 // to registers, 32 (d = 64: 64) at a time, the next ones' keys while the
 // values of these are used and the other way round; nothing is staged, no warp
 // waits for another before its tokens are done.  Measured: 4 sequences of
-// 131072 tokens, 8 kv heads of 128, G = 4: 172 us, 6.2 TB/s, and 180 once the
-// card is at its power limit (a tenth of a second on); 32 of 4000 to 8192 with
+// 131072 tokens, 8 kv heads of 128, G = 4: 172 us, 6.2 TB/s, and 180 to 190
+// once the card is at its power limit (a tenth of a second on); 32 of 4000 to 8192 with
 // weights 86 us; G = 16 244 us, 4.4 TB/s, bound by the latency of 8 warps an
 // SM; more heads read the cache once per 16 of them (32 heads over one kv head,
 // 16 x 32768 tokens: 71 us, a reading is 20).
@@ -455,14 +455,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint4 ldg_stream16(const uint8_t* p) {
+// Tokens on their way through the registers: read once, and like ld_behind
+// loaded behind the wait.
+__device__ __forceinline__ uint4 ld_stream16(const uint8_t* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
 }
-__device__ __forceinline__ uint2 ldg_stream8(const uint8_t* p) {
+__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
   uint2 r;
   asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
                : "=r"(r.x), "=r"(r.y)
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
-            kw[i][r][x] = ldg_stream16(base + (koff + (16 * i + 8 * r) * st + 64 * x));
+            kw[i][r][x] = ld_stream16(base + (koff + (16 * i + 8 * r) * st + 64 * x));
     } else {
 #pragma unroll
       for (int i = 0; i < NG; ++i)
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
           for (int x = 0; x < D / 64; ++x) {
             kw[i][r][x] = make_uint4(0, 0, 0, 0);
             if (first + 16 * i + 8 * r + gr < len)
-              kw[i][r][x] = ldg_stream16(base + (koff + (16 * i + 8 * r) * st + 64 * x));
+              kw[i][r][x] = ld_stream16(base + (koff + (16 * i + 8 * r) * st + 64 * x));
           }
     }
 #pragma unroll
@@ -586,13 +588,13 @@ __global__ void __launch_bounds__(32 * W, SOLE ? 1 : kv8_dec_ctas(NT))
     const uint8_t* base = vb + (int64_t)first * p.g.st;
     auto one = [&](uint32_t (&w)[VW], uint32_t off) {
       if constexpr (D == 128) {
-        const uint4 x = ldg_stream16(base + off);
+        const uint4 x = ld_stream16(base + off);
         w[0] = x.x;
         w[1] = x.y;
         w[2] = x.z;
         w[3] = x.w;
       } else {
-        const uint2 x = ldg_stream8(base + off);
+        const uint2 x = ld_stream8(base + off);
         w[0] = x.x;
         w[1] = x.y;
       }
@@ -1320,7 +1322,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_gather_kernel(
     w[p] = make_uint4(0, 0, 0, 0);
     s[p] = 0.0f;
     if (src[p] >= 0) {
-      w[p] = ldg_stream16(codes + src[p] * g.st);
+      w[p] = ld_stream16(codes + src[p] * g.st);
       s[p] = __ldg(scales + (src[p] >> lb));
     }
   }
